@@ -230,7 +230,7 @@ def _decode_own(s):
 
 def _append_own(s):
     c = s["case"]
-    ws = _ws(s, tri.tri_append_paged_workspace_bytes())
+    ws = _ws(s, tri.tri_append_paged_workspace_bytes(s["table"].shape[0]))
     tri.tri_append_paged(s["k"], s["v"], s["pos"], s["table"], c["n_seq"], c["n_layers"], c["kv"], s["n_valid"],
                          s["k_new"], s["v_new"], s["pos_new"], n_add=s["n_add"], page_refs=s["refs"],
                          p_cur=s["p_cur"], ws=ws)
