@@ -101,6 +101,8 @@ typedef enum tri_dtype {
 #define TRI_FLAG_INDEX_RANGE 0x2u  /* a kept index outside [0, cap_src) or n_kept > B; row skipped */
 #define TRI_FLAG_NONFINITE 0x4u    /* a final score was NaN (ranked last) */
 #define TRI_FLAG_TIMEOUT 0x8u      /* a bounded wait inside a kernel gave up */
+#define TRI_FLAG_NO_PAGES 0x10u    /* the pool has fewer free pages than a call needs; none were taken */
+#define TRI_FLAG_SHARED_PAGE 0x20u /* rows would have been written into a shared page; unit left as it is */
 
 #define TRI_MAX_OFFSETS 64
 #define TRI_MAX_GROUP 8
@@ -520,6 +522,137 @@ tri_status tri_append(void* k_cache, void* v_cache, int32_t* pos_cache, tri_dtyp
                       int32_t* n_valid, int64_t* p_cur, const void* k_new, const void* v_new,
                       const int32_t* pos_new, int64_t n_new, void* ws, size_t ws_bytes,
                       void* stream);
+
+/* ---------------------------------------------------------------------- */
+/* Paged cache: decode attention, append, pages                            */
+/* ---------------------------------------------------------------------- */
+
+/*
+ * The calls below work on the paged cache of tri_prune_paged_inplace: K and V
+ * pools [n_pages][page_rows][head_dim] (dt) and a device page table
+ * [n_units][pages_per_unit] int32, entry -1 where a unit has no page; row j of
+ * unit u is row j % page_rows of page page_table[u][j / page_rows].  page_rows
+ * is any number >= 1 here (the prune wants a multiple of 128), n_pages *
+ * page_rows and n_units * pages_per_unit at most 2^31 - 1.  An entry below
+ * -1 or >= n_pages sets TRI_FLAG_INDEX_RANGE where it is met and counts as no
+ * page.  page_refs (device, [n_pages] int32) counts the table entries that
+ * name a page; 0: the page is free.  The caller starts with a table of -1 and
+ * counts of 0 and leaves both to tri_pages_fit, tri_pages_fork and
+ * tri_pages_compact.  A serving step is
+ *   tri_pages_fit (n_new = 1), per layer tri_append_paged and
+ *   tri_decode_attention_paged; every 128 tokens tri_pages_fit (own = 1),
+ *   tri_prune_paged_inplace and, with n_valid = n_kept, tri_pages_fit
+ *   (n_new = 0), which frees the pages that the prune emptied.
+ * layer: -1 takes every unit, u = (seq * n_layers + layer) * n_kvheads + head;
+ * 0 .. n_layers-1 only that layer's units, and the per-unit arrays of the call
+ * (q, out, lse; k_new, v_new, pos_new) then hold [n_seq][n_kvheads] units.  The
+ * table, n_valid and pos always hold all units.
+ * Every result, the page numbers included, depends on the arguments alone.
+ */
+
+/* Workspace bytes of tri_decode_attention_paged for `n_units` units of the
+ * call (of one layer: n_seq * n_kvheads). */
+size_t tri_decode_paged_workspace_bytes(int64_t n_units, int G);
+
+/*
+ * tri_decode_attention through the page table: attention of the next token
+ * over each unit's first n_valid rows, split over the rows and joined.
+ *   q: [units][G][head_dim] (dt); scale > 0; out: [units][G][head_dim] float32.
+ *   n_valid: [n_units], rows of every unit (pages_per_unit * page_rows at most).
+ *   lse: out, nullable, [units][G] float32: log sum_j exp(s_j), -inf for a unit
+ *   without rows (whose out is zeros), for joining with attention over other
+ *   keys.  Rows of a missing page carry no weight (TRI_FLAG_INDEX_RANGE).
+ */
+tri_status tri_decode_attention_paged(const void* q, const void* k_pool, const void* v_pool,
+                                      tri_dtype dt, int64_t n_seq, int64_t n_layers,
+                                      int64_t n_kvheads, int64_t layer, int G, int head_dim,
+                                      const int32_t* page_table, int64_t page_rows,
+                                      int64_t pages_per_unit, int64_t n_pages,
+                                      const int32_t* n_valid, float scale, float* out, float* lse,
+                                      void* ws, size_t ws_bytes, void* stream);
+
+/* Workspace bytes of tri_append_paged for `n_units` units of the call. */
+size_t tri_append_paged_workspace_bytes(int64_t n_units);
+
+/*
+ * tri_append through the page table: rows n_valid[u] .. n_valid[u]+add-1 of
+ * unit u receive the first add = n_add[seq] of its n_new new rows (n_add
+ * NULL: all of them); n_valid[u] grows by add and p_cur[seq] (nullable)
+ * becomes max(p_cur[seq], 1 + the largest new position).  The rows of a
+ * padded batch past n_add[seq] are not read.
+ *   v_pool with v_new, and pos ([n_units][cap]) with pos_new, may be NULL;
+ *   cap <= pages_per_unit * page_rows bounds the rows of a unit.
+ *   page_refs (nullable): counts of tri_pages_fit; without them no page may
+ *   be shared.
+ * A unit whose rows do not fit in cap (TRI_FLAG_NVALID_RANGE), whose pages for
+ * the new rows are not all there (TRI_FLAG_INDEX_RANGE) or one of them shared
+ * (TRI_FLAG_SHARED_PAGE) is left unchanged.  The new rows must not overlap
+ * the pools.
+ */
+tri_status tri_append_paged(void* k_pool, void* v_pool, int32_t* pos, tri_dtype dt, int64_t n_seq,
+                            int64_t n_layers, int64_t n_kvheads, int64_t layer, int64_t cap,
+                            int head_dim, const int32_t* page_table, int64_t page_rows,
+                            int64_t pages_per_unit, int64_t n_pages, const int32_t* page_refs,
+                            int32_t* n_valid, int64_t* p_cur, const void* k_new, const void* v_new,
+                            const int32_t* pos_new, const int32_t* n_add, int64_t n_new, void* ws,
+                            size_t ws_bytes, void* stream);
+
+/* Workspace bytes of tri_pages_fit, tri_pages_fork and tri_pages_compact. */
+size_t tri_pages_workspace_bytes(int64_t n_units, int64_t pages_per_unit, int64_t n_pages);
+
+/*
+ * Make every unit hold exactly the pages that its n_valid rows and the next
+ * add = n_add[seq] rows (n_add NULL: n_new; n_add[seq] <= n_new) need, each
+ * page that the next rows go into its own:
+ *   1. pages of slots behind the last row are given back (entry -1, count - 1);
+ *   2. slots without a page get one, and slots whose page is shared (count
+ *      > 1) and holds a row >= n_valid[u] to be added get a copy of it, rows
+ *      below n_valid included.  own != 0: every shared page is copied (before
+ *      an in-place prune, which rewrites all rows).  Where all holders of a
+ *      page ask for a copy, the last of them keeps the page.
+ * The i-th request in (unit, slot) order gets the i-th free page of the pool.
+ * With fewer free pages than requests none is served (the pages of step 1
+ * stay free) and TRI_FLAG_NO_PAGES is set.
+ *   v_pool: nullable.  n_free: out, nullable, device int32: free pages after
+ *   the call; below 0, minus the pages that were lacking.
+ * Errors on the device: n_valid outside [0, pages_per_unit * page_rows], or
+ * more rows than that with the added ones (TRI_FLAG_NVALID_RANGE; clamped).
+ */
+tri_status tri_pages_fit(void* k_pool, void* v_pool, tri_dtype dt, int64_t n_seq, int64_t n_units,
+                         int head_dim, int32_t* page_table, int64_t page_rows,
+                         int64_t pages_per_unit, int64_t n_pages, int32_t* page_refs,
+                         const int32_t* n_valid, const int32_t* n_add, int64_t n_new, int own,
+                         int32_t* n_free, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Sequence dst_seq[i] becomes a continuation of sequence src_seq[i], for all
+ * i < n_fork at once: sources are read as they were on entry, so beams may
+ * change places.  The units of dst share the pages that hold src's n_valid
+ * rows (count + 1; no row is copied: tri_pages_fit copies what will be
+ * written), dst's old pages are given back, and n_valid, the first n_valid
+ * positions of pos ([n_units][cap], nullable) and p_cur ([n_seq], nullable)
+ * are copied.  src_seq[i] = -1 empties dst (n_valid and p_cur 0).
+ *   src_seq, dst_seq: device [n_fork] int32, n_fork <= 1024.
+ * A fork with an index out of range, or whose dst_seq an earlier one has, is
+ * skipped and sets TRI_FLAG_INDEX_RANGE.
+ */
+tri_status tri_pages_fork(int32_t* page_table, int64_t page_rows, int64_t pages_per_unit,
+                          int64_t n_pages, int32_t* page_refs, int64_t n_seq, int64_t n_units,
+                          const int32_t* src_seq, const int32_t* dst_seq, int64_t n_fork,
+                          int32_t* n_valid, int32_t* pos, int64_t cap, int64_t* p_cur, void* ws,
+                          size_t ws_bytes, void* stream);
+
+/*
+ * Move the pool's n_live pages in use to its front: the i-th used page at or
+ * behind n_live goes to the i-th free page before it, table entries and
+ * counts follow, and pages n_live .. n_pages-1 are free afterwards (the pool
+ * can be cut there).
+ *   v_pool: nullable.  n_live: out, nullable, device int32.
+ */
+tri_status tri_pages_compact(void* k_pool, void* v_pool, tri_dtype dt, int64_t n_units,
+                             int head_dim, int32_t* page_table, int64_t page_rows,
+                             int64_t pages_per_unit, int64_t n_pages, int32_t* page_refs,
+                             int32_t* n_live, void* ws, size_t ws_bytes, void* stream);
 
 /* ---------------------------------------------------------------------- */
 /* Launch accounting (profiling)                                           */

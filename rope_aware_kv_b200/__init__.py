@@ -36,6 +36,8 @@ FLAG_NVALID_RANGE = 0x1
 FLAG_INDEX_RANGE = 0x2
 FLAG_NONFINITE = 0x4
 FLAG_TIMEOUT = 0x8
+FLAG_NO_PAGES = 0x10
+FLAG_SHARED_PAGE = 0x20
 
 MAX_OFFSETS = 64
 HEAD_DIM = 128
@@ -60,6 +62,9 @@ EXPORTS = (
     "tri_compact_inplace", "tri_prune_inplace", "tri_calibrate_ex",
     "tri_decode_workspace_bytes", "tri_decode_attention",
     "tri_logit_reconstruct", "tri_logit_curve", "tri_pearson", "tri_prune_paged_inplace",
+    "tri_decode_paged_workspace_bytes", "tri_decode_attention_paged",
+    "tri_append_paged_workspace_bytes", "tri_append_paged",
+    "tri_pages_workspace_bytes", "tri_pages_fit", "tri_pages_fork", "tri_pages_compact",
 )
 
 
@@ -132,6 +137,18 @@ def load(path: Optional[str] = None):
                             P, i64, P, P, P, i64, P, P, P, P, sz, P]),
         "tri_append": (i32, [P, P, P, i32, i64, i64, i64, i32, P, P, P, P, P, i64, P, sz, P]),
         "tri_check_device_error": (i32, [P, P, u32p]),
+        "tri_decode_paged_workspace_bytes": (sz, [i64, i32]),
+        "tri_decode_attention_paged": (i32, [P, P, P, i32, i64, i64, i64, i64, i32, i32, P, i64,
+                                             i64, i64, P, ctypes.c_float, P, P, P, sz, P]),
+        "tri_append_paged_workspace_bytes": (sz, [i64]),
+        "tri_append_paged": (i32, [P, P, P, i32, i64, i64, i64, i64, i64, i32, P, i64, i64, i64, P,
+                                   P, P, P, P, P, P, i64, P, sz, P]),
+        "tri_pages_workspace_bytes": (sz, [i64, i64, i64]),
+        "tri_pages_fit": (i32, [P, P, i32, i64, i64, i32, P, i64, i64, i64, P, P, P, i64, i32, P, P,
+                                sz, P]),
+        "tri_pages_fork": (i32, [P, i64, i64, i64, P, i64, i64, P, P, i64, P, P, i64, P, P, sz,
+                                 P]),
+        "tri_pages_compact": (i32, [P, P, i32, i64, i32, P, i64, i64, i64, P, P, P, sz, P]),
         "tri_set_timing_events": (i32, [ctypes.POINTER(ctypes.c_void_p), i32]),
         "tri_last_launch_count": (i32, []),
         "tri_set_phase_trace": (i32, [P, sz]),
@@ -537,6 +554,235 @@ def tri_append(k_cache, v_cache, pos_cache, n_seq: int, n_valid: torch.Tensor,
         _ptr(k_cache), _ptr(v_cache), _ptr(pos_cache), _dt(k_cache), n_seq, U, cap, d,
         _ptr(n_valid), _ptr(p_cur), _ptr(k_new), _ptr(v_new), _ptr(pos_new), n_new, _ptr(ws),
         ws.numel(), _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
+# paged cache: decode attention, append, pages
+# ---------------------------------------------------------------------------
+# Pools [n_pages, page_rows, d], page table int32 [n_units, pages_per_unit]
+# (-1: no page), page_refs int32 [n_pages] (table entries that name a page);
+# units in the order [n_seq][n_layers][n_kvheads].
+
+class _PagedCall:
+    """Shape, type and device checks of one paged call, and the device, stream
+    and workspace that it runs with."""
+
+    def __init__(self, page_table: torch.Tensor, stream):
+        if not page_table.is_cuda:
+            raise ValueError("libtri takes CUDA tensors")
+        self.dev = page_table.device
+        self.stream = stream
+        self.n_units, self.per_unit = self.ints("page_table", page_table, 2).shape
+
+    def ints(self, name, t, dims=1, shape=None):
+        return self.check(name, t, torch.int32, dims, shape)
+
+    def check(self, name, t, dtype, dims, shape=None):
+        if t is None:
+            return None
+        if t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.dim() != dims or (shape is not None and tuple(t.shape) != tuple(shape)):
+            raise ValueError(f"{name} must have shape {shape or f'of {dims} dimensions'}, "
+                             f"got {tuple(t.shape)}")
+        if t.device != self.dev:
+            raise ValueError(f"{name} must be on {self.dev}, got {t.device}")
+        if not t.is_contiguous():
+            raise ValueError("libtri takes contiguous tensors")
+        return t
+
+    def pools(self, k_pool, v_pool):
+        _dt(k_pool)
+        self.check("k_pool", k_pool, k_pool.dtype, 3)
+        self.check("v_pool", v_pool, k_pool.dtype, 3, k_pool.shape)
+        return k_pool.shape
+
+    def units(self, n_seq, n_layers, n_kvheads):
+        if n_seq * n_layers * n_kvheads != self.n_units:
+            raise ValueError(f"page_table has {self.n_units} units, not {n_seq} x {n_layers} x "
+                             f"{n_kvheads}")
+
+    def empty(self, shape, dtype):
+        with self.on_stream():
+            return torch.empty(shape, dtype=dtype, device=self.dev)
+
+    def on_stream(self):
+        """The call's stream as the current one: a buffer made under it is
+        not handed out again before the call is done with it."""
+        return torch.cuda.stream(self.stream)
+
+    def run(self, name, nbytes, ws, args):
+        if ws is None:
+            ws = self.empty(max(int(nbytes), 256), torch.uint8)
+        elif ws.device != self.dev or not ws.is_contiguous():
+            raise ValueError(f"ws must be a contiguous tensor on {self.dev}")
+        fn = getattr(load(), name)
+        args = (*args, ctypes.c_void_p(ws.data_ptr()), ws.numel() * ws.element_size())
+        if self.dev.index == torch.cuda.current_device():
+            s = self.stream if self.stream is not None else torch.cuda.current_stream()
+            _check(name, fn(*args, ctypes.c_void_p(s.cuda_stream)))
+        else:
+            with torch.cuda.device(self.dev):
+                s = self.stream if self.stream is not None else torch.cuda.current_stream()
+                _check(name, fn(*args, ctypes.c_void_p(s.cuda_stream)))
+
+
+def _p(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _layer(layer: Optional[int]) -> int:
+    return -1 if layer is None else int(layer)
+
+
+def tri_decode_paged_workspace_bytes(n_units: int, G: int) -> int:
+    return load().tri_decode_paged_workspace_bytes(n_units, G)
+
+
+def tri_decode_attention_paged(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor,
+                               page_table: torch.Tensor, n_seq: int, n_layers: int,
+                               n_kvheads: int, n_valid: torch.Tensor,
+                               layer: Optional[int] = None, scale: Optional[float] = None,
+                               out: Optional[torch.Tensor] = None,
+                               lse: Optional[torch.Tensor] = None,
+                               ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Attention of one query token per head over each unit's first n_valid
+    rows of a paged cache: q [units, G, d] -> out [units, G, d] float32 (and
+    ``lse`` [units, G] float32, the logarithm of each softmax's denominator).
+    The units are all n_seq * n_layers * n_kvheads (``layer`` None or -1) or
+    one layer's n_seq * n_kvheads; page_table and n_valid hold all of them."""
+    c = _PagedCall(page_table, stream)
+    n_pages, page_rows, d = c.pools(k_pool, v_pool)
+    c.units(n_seq, n_layers, n_kvheads)
+    layer = _layer(layer)
+    U = n_seq * n_kvheads * (n_layers if layer < 0 else 1)
+    G = q.shape[1] if q.dim() == 3 else 0
+    c.check("q", q, k_pool.dtype, 3, (U, G, d))
+    c.ints("n_valid", n_valid, shape=(c.n_units,))
+    if out is None:
+        out = c.empty((U, G, d), torch.float32)
+    c.check("out", out, torch.float32, 3, (U, G, d))
+    c.check("lse", lse, torch.float32, 2, (U, G))
+    sc = (1.0 / d ** 0.5) if scale is None else float(scale)
+    c.run("tri_decode_attention_paged", 0 if ws is not None else tri_decode_paged_workspace_bytes(U, G),
+          ws, (_p(q), _p(k_pool), _p(v_pool), _dt(k_pool), n_seq, n_layers, n_kvheads, layer, G, d,
+               _p(page_table), page_rows, c.per_unit, n_pages, _p(n_valid), sc, _p(out), _p(lse)))
+    return out
+
+
+def tri_append_paged_workspace_bytes(n_units: int) -> int:
+    return load().tri_append_paged_workspace_bytes(n_units)
+
+
+def tri_append_paged(k_pool: torch.Tensor, v_pool: Optional[torch.Tensor],
+                     pos: Optional[torch.Tensor], page_table: torch.Tensor, n_seq: int,
+                     n_layers: int, n_kvheads: int, n_valid: torch.Tensor, k_new: torch.Tensor,
+                     v_new: Optional[torch.Tensor], pos_new: Optional[torch.Tensor],
+                     layer: Optional[int] = None, n_add: Optional[torch.Tensor] = None,
+                     page_refs: Optional[torch.Tensor] = None,
+                     p_cur: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
+                     stream=None):
+    """Append the first n_add[seq] (None: all) of the new rows k_new / v_new
+    [units, n_new, d], pos_new [units, n_new] to each unit of a paged cache;
+    n_valid grows and p_cur [n_seq] int64 rises in place.  The pages must be
+    there and unshared (``tri_pages_fit``); a unit that cannot take its rows is
+    left as it is and sets a device flag."""
+    c = _PagedCall(page_table, stream)
+    n_pages, page_rows, d = c.pools(k_pool, v_pool)
+    c.units(n_seq, n_layers, n_kvheads)
+    layer = _layer(layer)
+    U = n_seq * n_kvheads * (n_layers if layer < 0 else 1)
+    n_new = k_new.shape[1] if k_new.dim() == 3 else 0
+    c.check("k_new", k_new, k_pool.dtype, 3, (U, n_new, d))
+    c.check("v_new", v_new, k_pool.dtype, 3, (U, n_new, d))
+    c.ints("pos_new", pos_new, 2, (U, n_new))
+    c.ints("pos", pos, 2)
+    if pos is not None and pos.shape[0] != c.n_units:
+        raise ValueError(f"pos must have {c.n_units} rows, got {pos.shape[0]}")
+    cap = c.per_unit * page_rows if pos is None else pos.shape[1]
+    c.ints("n_valid", n_valid, shape=(c.n_units,))
+    c.ints("n_add", n_add, shape=(n_seq,))
+    c.ints("page_refs", page_refs, shape=(n_pages,))
+    c.check("p_cur", p_cur, torch.int64, 1, (n_seq,))
+    c.run("tri_append_paged", 0 if ws is not None else tri_append_paged_workspace_bytes(U), ws,
+          (_p(k_pool), _p(v_pool), _p(pos), _dt(k_pool), n_seq, n_layers, n_kvheads, layer, cap, d,
+           _p(page_table), page_rows, c.per_unit, n_pages, _p(page_refs), _p(n_valid), _p(p_cur),
+           _p(k_new), _p(v_new), _p(pos_new), _p(n_add), n_new))
+
+
+def tri_pages_workspace_bytes(n_units: int, pages_per_unit: int, n_pages: int) -> int:
+    return load().tri_pages_workspace_bytes(n_units, pages_per_unit, n_pages)
+
+
+def _pages_ws_bytes(c: _PagedCall, n_pages: int, ws) -> int:
+    return 0 if ws is not None else tri_pages_workspace_bytes(c.n_units, c.per_unit, n_pages)
+
+
+def tri_pages_fit(k_pool: torch.Tensor, v_pool: Optional[torch.Tensor], page_table: torch.Tensor,
+                  page_refs: torch.Tensor, n_seq: int, n_valid: torch.Tensor, n_new: int = 0,
+                  n_add: Optional[torch.Tensor] = None, own: bool = False,
+                  n_free: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
+                  stream=None) -> torch.Tensor:
+    """Give every unit exactly the pages that its n_valid rows and the next
+    n_add[seq] (None: n_new) rows need: pages behind them are freed, missing
+    ones taken from the pool, shared ones that will be written (``own``: every
+    shared one) copied.  Returns ``n_free`` (int32 CUDA tensor [1]): the free
+    pages left, or below 0 minus the pages lacking, when nothing was taken."""
+    c = _PagedCall(page_table, stream)
+    n_pages, page_rows, d = c.pools(k_pool, v_pool)
+    c.ints("page_refs", page_refs, shape=(n_pages,))
+    c.ints("n_valid", n_valid, shape=(c.n_units,))
+    c.ints("n_add", n_add, shape=(n_seq,))
+    if n_free is None:
+        n_free = c.empty((1,), torch.int32)
+    c.ints("n_free", n_free, shape=(1,))
+    c.run("tri_pages_fit", _pages_ws_bytes(c, n_pages, ws), ws,
+          (_p(k_pool), _p(v_pool), _dt(k_pool), n_seq, c.n_units, d, _p(page_table), page_rows,
+           c.per_unit, n_pages, _p(page_refs), _p(n_valid), _p(n_add), int(n_new), int(bool(own)),
+           _p(n_free)))
+    return n_free
+
+
+def tri_pages_fork(page_table: torch.Tensor, page_refs: torch.Tensor, page_rows: int, n_seq: int,
+                   n_valid: torch.Tensor, src_seq: torch.Tensor, dst_seq: torch.Tensor,
+                   pos: Optional[torch.Tensor] = None, p_cur: Optional[torch.Tensor] = None,
+                   ws: Optional[torch.Tensor] = None, stream=None):
+    """Sequence dst_seq[i] becomes a continuation of src_seq[i] (-1: empty),
+    for all i at once, sharing its pages; n_valid, pos [n_units, cap] and
+    p_cur [n_seq] int64 follow.  Shared pages are copied by ``tri_pages_fit``
+    when they are about to be written."""
+    c = _PagedCall(page_table, stream)
+    n_pages = c.ints("page_refs", page_refs).shape[0]
+    c.ints("n_valid", n_valid, shape=(c.n_units,))
+    n_fork = c.ints("src_seq", src_seq).shape[0]
+    c.ints("dst_seq", dst_seq, shape=(n_fork,))
+    c.ints("pos", pos, 2)
+    if pos is not None and pos.shape[0] != c.n_units:
+        raise ValueError(f"pos must have {c.n_units} rows, got {pos.shape[0]}")
+    c.check("p_cur", p_cur, torch.int64, 1, (n_seq,))
+    c.run("tri_pages_fork", _pages_ws_bytes(c, n_pages, ws), ws,
+          (_p(page_table), int(page_rows), c.per_unit, n_pages, _p(page_refs), n_seq, c.n_units,
+           _p(src_seq), _p(dst_seq), n_fork, _p(n_valid), _p(pos),
+           0 if pos is None else pos.shape[1], _p(p_cur)))
+
+
+def tri_pages_compact(k_pool: torch.Tensor, v_pool: Optional[torch.Tensor],
+                      page_table: torch.Tensor, page_refs: torch.Tensor,
+                      n_live: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
+                      stream=None) -> torch.Tensor:
+    """Move the pages in use to the front of the pool, tables and counts with
+    them.  Returns ``n_live`` (int32 CUDA tensor [1]), the number of pages in
+    use: those from there on are free."""
+    c = _PagedCall(page_table, stream)
+    n_pages, page_rows, d = c.pools(k_pool, v_pool)
+    c.ints("page_refs", page_refs, shape=(n_pages,))
+    if n_live is None:
+        n_live = c.empty((1,), torch.int32)
+    c.ints("n_live", n_live, shape=(1,))
+    c.run("tri_pages_compact", _pages_ws_bytes(c, n_pages, ws), ws,
+          (_p(k_pool), _p(v_pool), _dt(k_pool), c.n_units, d, _p(page_table), page_rows, c.per_unit,
+           n_pages, _p(page_refs), _p(n_live)))
+    return n_live
 
 
 def tri_set_timing_events(events: Optional[Sequence["torch.cuda.Event"]]):

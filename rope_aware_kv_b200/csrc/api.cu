@@ -13,6 +13,7 @@
 #include "tri_internal.cuh"
 #include "tri_launch.h"
 #include "calibrate_dp.h"
+#include "paged.h"
 
 using namespace tri;
 
@@ -510,6 +511,88 @@ struct LaunchScope {
 
 char* ws_at(void* ws, size_t off) { return static_cast<char*>(ws) + off; }
 uint32_t* ws_flag(void* ws) { return reinterpret_cast<uint32_t*>(ws); }
+
+// Sizes of a paged cache (the paged calls).
+tri_status check_paged(tri_dtype dt, int head_dim, int64_t n_seq, int64_t n_units,
+                       const void* page_table, int64_t page_rows, int64_t pages_per_unit,
+                       int64_t n_pages) {
+    if (!page_table || !aligned4(page_table) || n_seq < 1 || n_units < 1 || n_units % n_seq != 0 ||
+        page_rows < 1 || pages_per_unit < 1 || n_pages < 1)
+        return TRI_ERR_INVALID_ARG;
+    if (!dtype_ok(dt) || head_dim != kD) return TRI_ERR_UNSUPPORTED;
+    if (n_seq > INT32_MAX || n_units > INT32_MAX || page_rows > INT32_MAX / n_pages ||
+        pages_per_unit > INT32_MAX / n_units || pages_per_unit > INT32_MAX / page_rows)
+        return TRI_ERR_UNSUPPORTED;
+    return TRI_OK;
+}
+
+// Units [n_seq][n_layers][n_kvheads], or those of one layer.
+tri_status check_slice(int64_t n_seq, int64_t n_layers, int64_t n_kvheads, int64_t layer,
+                       UnitSlice* sl) {
+    if (n_seq < 1 || n_layers < 1 || n_kvheads < 1 || layer < -1 || layer >= n_layers)
+        return TRI_ERR_INVALID_ARG;
+    if (n_seq > INT32_MAX / n_layers || n_seq * n_layers > INT32_MAX / n_kvheads)
+        return TRI_ERR_UNSUPPORTED;
+    sl->n = n_seq * n_kvheads * (layer < 0 ? n_layers : 1);
+    sl->n_layers = n_layers;
+    sl->n_kvheads = n_kvheads;
+    sl->layer = layer;
+    return TRI_OK;
+}
+
+PagedCache paged_cache(const int32_t* table, int64_t page_rows, int64_t pages_per_unit,
+                       int64_t n_pages, int64_t n_seq, int64_t n_units) {
+    PagedCache pc;
+    pc.table = const_cast<int32_t*>(table);
+    pc.per_unit = pages_per_unit;
+    pc.rows = page_rows;
+    pc.n_pages = n_pages;
+    pc.n_seq = n_seq;
+    pc.n_units = n_units;
+    return pc;
+}
+
+struct DecodePagedWs {
+    size_t counters, zero_end, part, total;
+};
+DecodePagedWs decode_paged_ws(int64_t n_units, int G) {
+    DecodePagedWs w;
+    Carve c;
+    w.counters = c.take(static_cast<size_t>(n_units) * 4);
+    w.zero_end = c.off;
+    w.part = c.take(static_cast<size_t>(2 * decode_paged_ctas(static_cast<int>(sm_count_or_default()))) *
+                    G * (2 + kD) * 4);
+    w.total = c.off;
+    return w;
+}
+
+struct PagesWs {
+    size_t writers, last, zero_end, slot_counts, page_counts, totals, list[4], total;
+};
+PagesWs pages_ws(int64_t n_units, int64_t pages_per_unit, int64_t n_pages) {
+    PagesWs w;
+    const int64_t slots = n_units * pages_per_unit;
+    Carve c;
+    w.writers = c.take(static_cast<size_t>(n_pages) * 4);
+    w.last = c.take(static_cast<size_t>(n_pages) * 4);
+    w.zero_end = c.off;
+    w.slot_counts = c.take(static_cast<size_t>((slots + kPageChunk - 1) / kPageChunk) * 8);
+    w.page_counts = c.take(static_cast<size_t>((n_pages + kPageChunk - 1) / kPageChunk) * 4);
+    w.totals = c.take(8);
+    const size_t most = static_cast<size_t>(slots < n_pages ? slots : n_pages);
+    for (size_t& l : w.list) l = c.take(most * 4);
+    w.total = c.off;
+    return w;
+}
+
+tri_status check_pages_ws(const void* ws, size_t ws_bytes, const PagesWs& w) {
+    return !ws || !aligned16(ws) || ws_bytes < w.total ? TRI_ERR_WORKSPACE : TRI_OK;
+}
+
+// Bytes of a pool, for the overlap checks.
+size_t pool_bytes(tri_dtype dt, int64_t page_rows, int64_t n_pages) {
+    return static_cast<size_t>(page_rows * n_pages) * kD * (dt == TRI_BF16 ? 2 : 4);
+}
 
 }  // namespace
 
@@ -1130,6 +1213,218 @@ tri_status tri_append(void* k_cache, void* v_cache, int32_t* pos_cache, tri_dtyp
     if (n_new == 0) return TRI_OK;
     return cuda_status(launch_append(dt, k_cache, v_cache, pos_cache, n_seq, n_units, cap, n_valid,
                                      p_cur, k_new, v_new, pos_new, n_new, ws_flag(ws), s));
+}
+
+size_t tri_decode_paged_workspace_bytes(int64_t n_units, int G) {
+    if (n_units < 1 || n_units > INT32_MAX || G < 1 || G > TRI_MAX_GROUP) return kWsHeader;
+    return decode_paged_ws(n_units, G).total;
+}
+
+tri_status tri_decode_attention_paged(const void* q, const void* k_pool, const void* v_pool,
+                                      tri_dtype dt, int64_t n_seq, int64_t n_layers,
+                                      int64_t n_kvheads, int64_t layer, int G, int head_dim,
+                                      const int32_t* page_table, int64_t page_rows,
+                                      int64_t pages_per_unit, int64_t n_pages,
+                                      const int32_t* n_valid, float scale, float* out, float* lse,
+                                      void* ws, size_t ws_bytes, void* stream) {
+    LaunchScope scope_;
+    DecodePagedArgs a;
+    TRI_TRY(check_slice(n_seq, n_layers, n_kvheads, layer, &a.sl));
+    const int64_t U = n_seq * n_layers * n_kvheads;
+    TRI_TRY(check_paged(dt, head_dim, n_seq, U, page_table, page_rows, pages_per_unit, n_pages));
+    if (!q || !k_pool || !v_pool || !out || !n_valid || !(scale > 0.f) || !std::isfinite(scale))
+        return TRI_ERR_INVALID_ARG;
+    if (G < 1 || G > TRI_MAX_GROUP) return TRI_ERR_UNSUPPORTED;
+    if (!aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(out) ||
+        !aligned4(n_valid) || !aligned4(lse))
+        return TRI_ERR_INVALID_ARG;
+    const DecodePagedWs w = decode_paged_ws(a.sl.n, G);
+    if (!ws || !aligned16(ws) || ws_bytes < w.total) return TRI_ERR_WORKSPACE;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    a.q = q;
+    a.k = k_pool;
+    a.v = v_pool;
+    a.pc = paged_cache(page_table, page_rows, pages_per_unit, n_pages, n_seq, U);
+    a.n_valid = n_valid;
+    a.scale_log2 = scale * 1.4426950408889634f;
+    a.out = out;
+    a.lse = lse;
+    a.counters = reinterpret_cast<uint32_t*>(ws_at(ws, w.counters));
+    a.part = reinterpret_cast<float*>(ws_at(ws, w.part));
+    a.flag = ws_flag(ws);
+    TRI_CUDA(cudaMemsetAsync(ws, 0, w.zero_end, s));
+    return cuda_status(
+        launch_decode_paged(dt, G, a, static_cast<int>(sm_count_or_default()), s));
+}
+
+size_t tri_append_paged_workspace_bytes(int64_t n_units) {
+    if (n_units < 1 || n_units > INT32_MAX) return kWsHeader;
+    return kWsHeader + align_up(static_cast<size_t>(n_units) * 4);
+}
+
+tri_status tri_append_paged(void* k_pool, void* v_pool, int32_t* pos, tri_dtype dt, int64_t n_seq,
+                            int64_t n_layers, int64_t n_kvheads, int64_t layer, int64_t cap,
+                            int head_dim, const int32_t* page_table, int64_t page_rows,
+                            int64_t pages_per_unit, int64_t n_pages, const int32_t* page_refs,
+                            int32_t* n_valid, int64_t* p_cur, const void* k_new, const void* v_new,
+                            const int32_t* pos_new, const int32_t* n_add, int64_t n_new, void* ws,
+                            size_t ws_bytes, void* stream) {
+    LaunchScope scope_;
+    AppendPagedArgs a;
+    TRI_TRY(check_slice(n_seq, n_layers, n_kvheads, layer, &a.sl));
+    const int64_t U = n_seq * n_layers * n_kvheads;
+    TRI_TRY(check_paged(dt, head_dim, n_seq, U, page_table, page_rows, pages_per_unit, n_pages));
+    if (!k_pool || !n_valid || n_new < 0 || cap < 1 || cap > pages_per_unit * page_rows)
+        return TRI_ERR_INVALID_ARG;
+    if (n_new > 0 && (!k_new || (v_pool == nullptr) != (v_new == nullptr) ||
+                      (pos == nullptr) != (pos_new == nullptr) || (p_cur && !pos_new)))
+        return TRI_ERR_INVALID_ARG;
+    if (!aligned16(k_pool) || !aligned16(v_pool) || !aligned16(k_new) || !aligned16(v_new) ||
+        !aligned4(pos) || !aligned4(pos_new) || !aligned4(page_refs) || !aligned4(n_valid) ||
+        !aligned4(n_add) || (reinterpret_cast<uintptr_t>(p_cur) & 7))
+        return TRI_ERR_INVALID_ARG;
+    if (n_new > INT32_MAX / a.sl.n) return TRI_ERR_UNSUPPORTED;
+    const size_t pb = pool_bytes(dt, page_rows, n_pages);
+    const size_t nb = static_cast<size_t>(a.sl.n * n_new) * kD * (dt == TRI_BF16 ? 2 : 4);
+    const void* pools[2] = {k_pool, v_pool};
+    const void* news[2] = {k_new, v_new};
+    for (const void* p : pools)
+        for (const void* n : news)
+            if (p && n && overlaps(p, pb, n, nb)) return TRI_ERR_INVALID_ARG;
+    if (v_pool && overlaps(k_pool, pb, v_pool, pb)) return TRI_ERR_INVALID_ARG;
+    if (!ws || !aligned16(ws) || ws_bytes < tri_append_paged_workspace_bytes(a.sl.n))
+        return TRI_ERR_WORKSPACE;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    TRI_CUDA(cudaMemsetAsync(ws, 0, kWsHeader, s));
+    if (n_new == 0) return TRI_OK;
+    a.k = k_pool;
+    a.v = v_pool;
+    a.pos = pos;
+    a.cap = cap;
+    a.pc = paged_cache(page_table, page_rows, pages_per_unit, n_pages, n_seq, U);
+    a.refs = page_refs;
+    a.n_valid = n_valid;
+    a.p_cur = p_cur;
+    a.k_new = k_new;
+    a.v_new = v_new;
+    a.pos_new = pos_new;
+    a.n_add = n_add;
+    a.n_new = n_new;
+    a.first = reinterpret_cast<int32_t*>(ws_at(ws, kWsHeader));
+    a.flag = ws_flag(ws);
+    return cuda_status(launch_append_paged(dt, a, s));
+}
+
+size_t tri_pages_workspace_bytes(int64_t n_units, int64_t pages_per_unit, int64_t n_pages) {
+    if (n_units < 1 || pages_per_unit < 1 || n_pages < 1 || n_pages > INT32_MAX ||
+        n_units > INT32_MAX || pages_per_unit > INT32_MAX / n_units)
+        return kWsHeader;
+    return pages_ws(n_units, pages_per_unit, n_pages).total;
+}
+
+tri_status tri_pages_fit(void* k_pool, void* v_pool, tri_dtype dt, int64_t n_seq, int64_t n_units,
+                         int head_dim, int32_t* page_table, int64_t page_rows,
+                         int64_t pages_per_unit, int64_t n_pages, int32_t* page_refs,
+                         const int32_t* n_valid, const int32_t* n_add, int64_t n_new, int own,
+                         int32_t* n_free, void* ws, size_t ws_bytes, void* stream) {
+    LaunchScope scope_;
+    TRI_TRY(check_paged(dt, head_dim, n_seq, n_units, page_table, page_rows, pages_per_unit, n_pages));
+    if (!k_pool || !page_refs || !n_valid || n_new < 0 || n_new > INT32_MAX) return TRI_ERR_INVALID_ARG;
+    if (!aligned16(k_pool) || !aligned16(v_pool) || !aligned4(page_refs) || !aligned4(n_valid) ||
+        !aligned4(n_add) || !aligned4(n_free))
+        return TRI_ERR_INVALID_ARG;
+    const size_t pb = pool_bytes(dt, page_rows, n_pages);
+    if (v_pool && overlaps(k_pool, pb, v_pool, pb)) return TRI_ERR_INVALID_ARG;
+    const PagesWs w = pages_ws(n_units, pages_per_unit, n_pages);
+    TRI_TRY(check_pages_ws(ws, ws_bytes, w));
+    FitArgs a;
+    a.k = k_pool;
+    a.v = v_pool;
+    a.pc = paged_cache(page_table, page_rows, pages_per_unit, n_pages, n_seq, n_units);
+    a.refs = page_refs;
+    a.n_valid = n_valid;
+    a.n_add = n_add;
+    a.n_new = n_new;
+    a.own = own;
+    a.n_free = n_free;
+    a.writers = reinterpret_cast<uint32_t*>(ws_at(ws, w.writers));
+    a.last = reinterpret_cast<uint32_t*>(ws_at(ws, w.last));
+    a.slot_counts = reinterpret_cast<uint2*>(ws_at(ws, w.slot_counts));
+    a.page_counts = reinterpret_cast<uint32_t*>(ws_at(ws, w.page_counts));
+    a.need_slot = reinterpret_cast<int32_t*>(ws_at(ws, w.list[0]));
+    a.need_old = reinterpret_cast<int32_t*>(ws_at(ws, w.list[1]));
+    a.copy_rank = reinterpret_cast<int32_t*>(ws_at(ws, w.list[2]));
+    a.free_page = reinterpret_cast<int32_t*>(ws_at(ws, w.list[3]));
+    a.totals = reinterpret_cast<uint32_t*>(ws_at(ws, w.totals));
+    a.flag = ws_flag(ws);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    TRI_CUDA(cudaMemsetAsync(ws, 0, w.zero_end, s));
+    return cuda_status(launch_pages_fit(dt, a, static_cast<int>(sm_count_or_default()), s));
+}
+
+tri_status tri_pages_fork(int32_t* page_table, int64_t page_rows, int64_t pages_per_unit,
+                          int64_t n_pages, int32_t* page_refs, int64_t n_seq, int64_t n_units,
+                          const int32_t* src_seq, const int32_t* dst_seq, int64_t n_fork,
+                          int32_t* n_valid, int32_t* pos, int64_t cap, int64_t* p_cur, void* ws,
+                          size_t ws_bytes, void* stream) {
+    LaunchScope scope_;
+    TRI_TRY(check_paged(TRI_BF16, kD, n_seq, n_units, page_table, page_rows, pages_per_unit, n_pages));
+    if (!page_refs || !n_valid || n_fork < 0 || (n_fork > 0 && (!src_seq || !dst_seq)) ||
+        (pos && (cap < 1 || cap > pages_per_unit * page_rows)))
+        return TRI_ERR_INVALID_ARG;
+    if (n_fork > kMaxForks) return TRI_ERR_UNSUPPORTED;
+    if (!aligned4(page_refs) || !aligned4(n_valid) || !aligned4(src_seq) || !aligned4(dst_seq) ||
+        !aligned4(pos) || (reinterpret_cast<uintptr_t>(p_cur) & 7))
+        return TRI_ERR_INVALID_ARG;
+    TRI_TRY(check_pages_ws(ws, ws_bytes, pages_ws(n_units, pages_per_unit, n_pages)));
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    TRI_CUDA(cudaMemsetAsync(ws, 0, kWsHeader, s));
+    if (n_fork == 0) return TRI_OK;
+    ForkArgs a;
+    a.pc = paged_cache(page_table, page_rows, pages_per_unit, n_pages, n_seq, n_units);
+    a.refs = page_refs;
+    a.n_valid = n_valid;
+    a.pos = pos;
+    a.cap = pos ? cap : 0;
+    a.p_cur = p_cur;
+    a.src = src_seq;
+    a.dst = dst_seq;
+    a.n_fork = n_fork;
+    a.done = ws_flag(ws) + 1;
+    a.flag = ws_flag(ws);
+    return cuda_status(launch_pages_fork(a, s));
+}
+
+tri_status tri_pages_compact(void* k_pool, void* v_pool, tri_dtype dt, int64_t n_units,
+                             int head_dim, int32_t* page_table, int64_t page_rows,
+                             int64_t pages_per_unit, int64_t n_pages, int32_t* page_refs,
+                             int32_t* n_live, void* ws, size_t ws_bytes, void* stream) {
+    LaunchScope scope_;
+    TRI_TRY(check_paged(dt, head_dim, 1, n_units, page_table, page_rows, pages_per_unit, n_pages));
+    if (!k_pool || !page_refs) return TRI_ERR_INVALID_ARG;
+    if (!aligned16(k_pool) || !aligned16(v_pool) || !aligned4(page_refs) || !aligned4(n_live))
+        return TRI_ERR_INVALID_ARG;
+    const size_t pb = pool_bytes(dt, page_rows, n_pages);
+    if (v_pool && overlaps(k_pool, pb, v_pool, pb)) return TRI_ERR_INVALID_ARG;
+    const PagesWs w = pages_ws(n_units, pages_per_unit, n_pages);
+    TRI_TRY(check_pages_ws(ws, ws_bytes, w));
+    CompactPagesArgs a;
+    a.k = k_pool;
+    a.v = v_pool;
+    a.pc = paged_cache(page_table, page_rows, pages_per_unit, n_pages, 1, n_units);
+    a.refs = page_refs;
+    a.n_live = n_live;
+    a.page_counts = reinterpret_cast<uint32_t*>(ws_at(ws, w.page_counts));
+    // At most half of the pages move: both lists fit where tri_pages_fit
+    // keeps its marks, and the ranks in its second half.
+    a.from = reinterpret_cast<int32_t*>(ws_at(ws, w.writers));
+    a.to = a.from + n_pages / 2;
+    a.rank = reinterpret_cast<int32_t*>(ws_at(ws, w.last));
+    a.totals = reinterpret_cast<uint32_t*>(ws_at(ws, w.totals));
+    a.flag = ws_flag(ws);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    TRI_CUDA(cudaMemsetAsync(ws, 0, kWsHeader, s));
+    return cuda_status(launch_pages_compact(dt, a, static_cast<int>(sm_count_or_default()), s));
 }
 
 tri_status tri_set_timing_events(void* const* events, int n_events) {
