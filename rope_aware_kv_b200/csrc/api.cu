@@ -1252,9 +1252,17 @@ tri_status tri_decode_attention_paged(const void* q, const void* k_pool, const v
     a.counters = reinterpret_cast<uint32_t*>(ws_at(ws, w.counters));
     a.part = reinterpret_cast<float*>(ws_at(ws, w.part));
     a.flag = ws_flag(ws);
+    const int n_sm = static_cast<int>(sm_count_or_default());
+    // Whole 8-row swizzle atoms of a page can be loaded as tensor tiles.
+    const int box = dt == TRI_BF16 ? decode_paged_box_rows(page_rows) : 0;
+    CUtensorMap kmap, vmap;
+    if (box) {
+        TRI_TRY(make_key_map(&kmap, k_pool, dt, n_pages * page_rows, box));
+        TRI_TRY(make_key_map(&vmap, v_pool, dt, n_pages * page_rows, box));
+    }
     TRI_CUDA(cudaMemsetAsync(ws, 0, w.zero_end, s));
-    return cuda_status(
-        launch_decode_paged(dt, G, a, static_cast<int>(sm_count_or_default()), s));
+    return cuda_status(box ? launch_decode_paged_tc(G, kmap, vmap, box, a, n_sm, s)
+                           : launch_decode_paged_rows(dt, G, a, n_sm, s));
 }
 
 size_t tri_append_paged_workspace_bytes(int64_t n_units) {

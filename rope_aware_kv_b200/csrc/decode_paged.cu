@@ -265,7 +265,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) decode_paged_rows_kernel(const
                 }
             }
         }
-        if (!whole) join_split_unit<kRowThreads>(a, G, p, i, tile0, n_tiles);
+        if (!whole) join_split_unit<kRowThreads, 0>(a, G, p, i, tile0, n_tiles);
         __syncthreads();  // red is rewritten by the next unit
         t = tile0 + b1;
         tile0 += n_tiles;
@@ -302,8 +302,8 @@ static cudaError_t launch_rows_t(int G, const DecodePagedArgs& a, int n_sm, cuda
     }
 }
 
-cudaError_t launch_decode_paged(tri_dtype dt, int G, const DecodePagedArgs& a, int n_sm,
-                                cudaStream_t s) {
+cudaError_t launch_decode_paged_rows(tri_dtype dt, int G, const DecodePagedArgs& a, int n_sm,
+                                     cudaStream_t s) {
     return dt == TRI_BF16 ? launch_rows_t<__nv_bfloat16>(G, a, n_sm, s)
                           : launch_rows_t<float>(G, a, n_sm, s);
 }

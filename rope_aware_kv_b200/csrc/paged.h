@@ -46,8 +46,18 @@ struct DecodePagedArgs {
     uint32_t* flag;
 };
 int decode_paged_ctas(int n_sm);
-cudaError_t launch_decode_paged(tri_dtype dt, int G, const DecodePagedArgs& a, int n_sm,
-                                cudaStream_t s);
+// Any page size, both types.
+cudaError_t launch_decode_paged_rows(tri_dtype dt, int G, const DecodePagedArgs& a, int n_sm,
+                                     cudaStream_t s);
+
+// decode_paged_tc.cu: bf16 pages of a multiple of 8 rows, through the tensor
+// cores.  kmap, vmap: the pools as rows of 128, boxes of 64 dims x box_rows
+// rows with a 128-byte swizzle.
+constexpr int kTcTile = 128;  // keys of one tile
+int decode_paged_box_rows(int64_t page_rows);  // 0: not served
+cudaError_t launch_decode_paged_tc(int G, const CUtensorMap& kmap, const CUtensorMap& vmap,
+                                   int box_rows, const DecodePagedArgs& a, int n_sm,
+                                   cudaStream_t s);
 
 // pages.cu
 struct AppendPagedArgs {

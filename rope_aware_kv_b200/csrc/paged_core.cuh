@@ -133,7 +133,8 @@ __device__ __forceinline__ float lse_of(float m, float l) {
 // and their (maximum, sum, accumulator) is written to this CTA's partial
 // slot.  The CTA that arrives last joins the unit's partials in CTA order:
 // out = sum_c 2^(m_c - M) acc_c / sum_c 2^(m_c - M) l_c.
-template <int kThreads>
+// Called by the kThreads threads of named barrier kBar.
+template <int kThreads, int kBar>
 __device__ void join_split_unit(const DecodePagedArgs& a, int G, const SplitPlan& p, int64_t i,
                                 int64_t tile0, int64_t n_tiles) {
     __shared__ bool last;
@@ -141,9 +142,9 @@ __device__ void join_split_unit(const DecodePagedArgs& a, int G, const SplitPlan
     const int c0 = cta_of_tile(p.total, p.ctas, tile0);
     const int c1 = cta_of_tile(p.total, p.ctas, tile0 + n_tiles - 1);
     __threadfence();
-    __syncthreads();
+    named_sync(kBar, kThreads);
     if (tid == 0) last = atomicAdd(a.counters + i, 1u) == static_cast<uint32_t>(c1 - c0);
-    __syncthreads();
+    named_sync(kBar, kThreads);
     if (!last) return;
     __threadfence();
     for (int e = tid; e < G * kD; e += kThreads) {
