@@ -553,15 +553,16 @@ PagedCache paged_cache(const int32_t* table, int64_t page_rows, int64_t pages_pe
 }
 
 struct DecodePagedWs {
-    size_t counters, zero_end, part, total;
+    size_t counters, zero_end, part, part_ml, total;
 };
 DecodePagedWs decode_paged_ws(int64_t n_units, int G) {
     DecodePagedWs w;
     Carve c;
     w.counters = c.take(static_cast<size_t>(n_units) * 4);
     w.zero_end = c.off;
-    w.part = c.take(static_cast<size_t>(2 * decode_paged_ctas(static_cast<int>(sm_count_or_default()))) *
-                    G * (2 + kD) * 4);
+    const size_t slots = 2 * decode_paged_ctas(static_cast<int>(sm_count_or_default()));
+    w.part = c.take(slots * G * kD * 4);
+    w.part_ml = c.take(slots * G * 8);
     w.total = c.off;
     return w;
 }
@@ -1251,6 +1252,7 @@ tri_status tri_decode_attention_paged(const void* q, const void* k_pool, const v
     a.lse = lse;
     a.counters = reinterpret_cast<uint32_t*>(ws_at(ws, w.counters));
     a.part = reinterpret_cast<float*>(ws_at(ws, w.part));
+    a.part_ml = reinterpret_cast<float2*>(ws_at(ws, w.part_ml));
     a.flag = ws_flag(ws);
     const int n_sm = static_cast<int>(sm_count_or_default());
     // Whole 8-row swizzle atoms of a page can be loaded as tensor tiles.

@@ -239,7 +239,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) decode_paged_rows_kernel(const
         }
         __syncthreads();
         const bool whole = b0 == 0 && b1 == n_tiles;
-        const int64_t slot = (static_cast<int64_t>(blockIdx.x) * 2 + (b0 == 0 && t != p.begin ? 1 : 0));
+        const int64_t slot = part_slot(p, blockIdx.x, tile0);
         for (int e = tid; e < G * kD; e += kRowThreads) {
             const int h = e / kD, d = e % kD;
             float M = -INFINITY;
@@ -257,15 +257,11 @@ __global__ void __launch_bounds__(kRowThreads, 1) decode_paged_rows_kernel(const
                 a.out[(i * G + h) * kD + d] = den == 0.f ? 0.f : num / den;
                 if (a.lse && d == 0) a.lse[i * G + h] = lse_of(M, den);
             } else {
-                float* x = a.part + (slot * G + h) * (2 + kD);
-                x[2 + d] = num;
-                if (d == 0) {
-                    x[0] = M;
-                    x[1] = den;
-                }
+                a.part[(slot * G + h) * kD + d] = num;
+                if (d == 0) a.part_ml[slot * G + h] = make_float2(M, den);
             }
         }
-        if (!whole) join_split_unit<kRowThreads, 0>(a, G, p, i, tile0, n_tiles);
+        if (!whole) join_split_unit<kRowWarps, 0, G>(a, p, i, tile0, n_tiles, red);
         __syncthreads();  // red is rewritten by the next unit
         t = tile0 + b1;
         tile0 += n_tiles;

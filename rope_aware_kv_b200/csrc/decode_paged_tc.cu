@@ -33,6 +33,7 @@ constexpr int kTcHalf = kTcTile * 128;     // 64 dims of the tile's rows: 16 KB
 constexpr int kTcMat = 2 * kTcHalf;        // K or V of a tile
 constexpr int kTcPRow = 64;                // bytes of a key's weights: 32 bf16
 
+// (q and p lie side by side: together they hold the joining of split units.)
 struct __align__(1024) TcShared {
     unsigned char k[kTcStages][kTcMat];
     unsigned char v[kTcStages][kTcMat];
@@ -154,10 +155,6 @@ decode_paged_tc_kernel(const __grid_constant__ CUtensorMap kmap,
         prefetch_tensormap(&vmap);
     }
     if (warp == 0) tc_alloc(&sm.tmem, 64);
-    // Weights' columns 24 .. 31 stay zero.
-    if (tid < kTcMath)
-        *reinterpret_cast<uint4*>(sm.p + tid * kTcPRow + ((3 ^ ((tid >> 1) & 3)) * 16)) =
-            make_uint4(0, 0, 0, 0);
     write_empty_units(a, G);
     tc_fence_before();
     const SplitPlan p = plan_split<kTcThreads>(a, kTcTile, 1);  // (synchronises the CTA)
@@ -229,7 +226,7 @@ decode_paged_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                 continue;
             }
             const int64_t t1 = min(tile0 + n_tiles, p.end);
-            const bool from_start = t == tile0, first_of_range = t == p.begin;
+            const bool from_start = t == tile0;
             // ---- Q, rows >= G zero; 16-byte chunk c of a 128-byte row r lies at c ^ (r & 7) ----
             for (int e = tid; e < 16 * 16; e += kTcMath) {
                 const int r = e >> 4, c = e & 15;
@@ -240,6 +237,9 @@ decode_paged_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                               c);
                 *reinterpret_cast<uint4*>(sm.q[c >> 3] + r * 128 + ((c & 7) ^ (r & 7)) * 16) = x;
             }
+            // Columns 24 .. 31 of the weights are zeros.
+            *reinterpret_cast<uint4*>(sm.p + tid * kTcPRow + ((3 ^ ((tid >> 1) & 3)) * 16)) =
+                make_uint4(0, 0, 0, 0);
             float m[G], l[G], acc[G];
 #pragma unroll
             for (int h = 0; h < G; ++h) {
@@ -372,7 +372,7 @@ decode_paged_tc_kernel(const __grid_constant__ CUtensorMap kmap,
             named_sync(1, kTcMath);
             if (*reinterpret_cast<volatile int*>(&sm.abort)) break;
             const bool whole = from_start && t1 == tile0 + n_tiles;
-            const int64_t slot = static_cast<int64_t>(blockIdx.x) * 2 + (from_start && !first_of_range ? 1 : 0);
+            const int64_t slot = part_slot(p, blockIdx.x, tile0);
 #pragma unroll
             for (int h = 0; h < G; ++h) {
                 const float den = (sm.wsum[0][h] + sm.wsum[1][h]) + (sm.wsum[2][h] + sm.wsum[3][h]);
@@ -380,15 +380,14 @@ decode_paged_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                     a.out[(i * G + h) * kD + tid] = den == 0.f ? 0.f : acc[h] / den;
                     if (a.lse && tid == 0) a.lse[i * G + h] = lse_of(m[h], den);
                 } else {
-                    float* x = a.part + (slot * G + h) * (2 + kD);
-                    x[2 + tid] = acc[h];
-                    if (tid == 0) {
-                        x[0] = m[h];
-                        x[1] = den;
-                    }
+                    a.part[(slot * G + h) * kD + tid] = acc[h];
+                    if (tid == 0) a.part_ml[slot * G + h] = make_float2(m[h], den);
                 }
             }
-            if (!whole) join_split_unit<kTcMath, 1>(a, G, p, i, tile0, n_tiles);
+            // (Q and P are free by now: every product of the unit is done.)
+            if (!whole)
+                join_split_unit<kTcMath / 32, 1, G>(a, p, i, tile0, n_tiles,
+                                                    reinterpret_cast<float*>(sm.q));
             named_sync(1, kTcMath);  // wsum and Q are rewritten by the next unit
             tile0 += n_tiles;
             ++i;
@@ -413,6 +412,8 @@ static cudaError_t launch_tc(const CUtensorMap& kmap, const CUtensorMap& vmap, i
                              const DecodePagedArgs& a, int n_sm, cudaStream_t s) {
     constexpr size_t smem = sizeof(TcShared) + 1024;
     static_assert(smem <= 227 * 1024, "tile ring too large");
+    static_assert(sizeof(TcShared::q) + sizeof(TcShared::p) >= (kTcMath / 32 - 1) * TRI_MAX_GROUP * kD * 4,
+                  "no room to join split units");
     auto* fn = decode_paged_tc_kernel<G>;
     cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(smem));

@@ -42,7 +42,10 @@ struct DecodePagedArgs {
     float* out;              // [sl.n][G][128]
     float* lse;              // [sl.n][G] or null
     uint32_t* counters;      // [sl.n], zero on entry: segments of a unit that are done
-    float* part;             // [2 * ctas][G][2 + 128] partial results of split units
+    // Partial results of split units, two slots a CTA: accumulators
+    // [2 * ctas][G][128] and (maximum, sum) [2 * ctas][G].
+    float* part;
+    float2* part_ml;
     uint32_t* flag;
 };
 int decode_paged_ctas(int n_sm);

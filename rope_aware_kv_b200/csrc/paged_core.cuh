@@ -121,50 +121,106 @@ __device__ __forceinline__ void write_empty_units(const DecodePagedArgs& a, int 
     }
 }
 
-__device__ __forceinline__ float ld_cg(const float* p) { return __ldcg(p); }
-
 // log2-domain running maximum and sum -> natural logarithm of the softmax's
 // denominator.
 __device__ __forceinline__ float lse_of(float m, float l) {
     return l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : (l == 0.f ? -INFINITY : l);
 }
 
-// The tiles [begin, end) of unit i (first tile tile0, n_tiles tiles) are done
-// and their (maximum, sum, accumulator) is written to this CTA's partial
-// slot.  The CTA that arrives last joins the unit's partials in CTA order:
-// out = sum_c 2^(m_c - M) acc_c / sum_c 2^(m_c - M) l_c.
-// Called by the kThreads threads of named barrier kBar.
-template <int kThreads, int kBar>
-__device__ void join_split_unit(const DecodePagedArgs& a, int G, const SplitPlan& p, int64_t i,
-                                int64_t tile0, int64_t n_tiles) {
+// Partial result of a unit's segment: slot 2 c of CTA c, or 2 c + 1 for a unit
+// that begins inside the CTA's range.
+__device__ __forceinline__ int64_t part_slot(const SplitPlan& p, int c, int64_t tile0) {
+    return 2 * static_cast<int64_t>(c) + (tile0 <= range_begin(p.total, p.ctas, c) ? 0 : 1);
+}
+
+// This CTA's partial of unit i (first tile tile0, n_tiles tiles) is written;
+// the CTA that arrives last joins the unit's partials in CTA order,
+//   out = sum_c 2^(m_c - M) acc_c / sum_c 2^(m_c - M) l_c.
+// Called by the kWarps * 32 threads of named barrier kBar.  A lane has 4 dims
+// of every head; the warps take the CTAs in turn, so the loads of a warp are
+// independent of one another, and are joined in warp order through red
+// ((kWarps - 1) * G * 128 floats of shared memory).
+template <int kWarps, int kBar, int G>
+__device__ void join_split_unit(const DecodePagedArgs& a, const SplitPlan& p, int64_t i,
+                                int64_t tile0, int64_t n_tiles, float* red) {
     __shared__ bool last;
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int c0 = cta_of_tile(p.total, p.ctas, tile0);
     const int c1 = cta_of_tile(p.total, p.ctas, tile0 + n_tiles - 1);
     __threadfence();
-    named_sync(kBar, kThreads);
+    named_sync(kBar, kWarps * 32);
     if (tid == 0) last = atomicAdd(a.counters + i, 1u) == static_cast<uint32_t>(c1 - c0);
-    named_sync(kBar, kThreads);
+    named_sync(kBar, kWarps * 32);
     if (!last) return;
     __threadfence();
-    for (int e = tid; e < G * kD; e += kThreads) {
-        const int h = e / kD, d = e % kD;
-        float M = -INFINITY;
-        for (int c = c0; c <= c1; ++c) {
-            const int slot = tile0 <= range_begin(p.total, p.ctas, c) ? 0 : 1;
-            M = fmaxf(M, ld_cg(a.part + ((static_cast<int64_t>(c) * 2 + slot) * G + h) * (2 + kD)));
+    float M[G], den[G];
+    float4 acc[G];
+#pragma unroll
+    for (int h = 0; h < G; ++h) {
+        M[h] = -INFINITY;
+        den[h] = 0.f;
+        acc[h] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    for (int c = c0 + lane; c <= c1; c += 32) {
+        const float2* ml = a.part_ml + part_slot(p, c, tile0) * G;
+#pragma unroll
+        for (int h = 0; h < G; ++h) M[h] = fmaxf(M[h], __ldcg(ml + h).x);
+    }
+#pragma unroll
+    for (int h = 0; h < G; ++h) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) M[h] = fmaxf(M[h], __shfl_xor_sync(0xffffffffu, M[h], o));
+    }
+    for (int cb = c0; cb <= c1; cb += 32) {
+        float w[G];
+        const bool in = cb + lane <= c1;
+        const float2* ml = a.part_ml + part_slot(p, in ? cb + lane : cb, tile0) * G;
+#pragma unroll
+        for (int h = 0; h < G; ++h) {
+            const float2 x = __ldcg(ml + h);
+            w[h] = in && x.x != -INFINITY ? exp2f(x.x - M[h]) : 0.f;
+            if (in) den[h] = fmaf(w[h], x.y, den[h]);
         }
-        float num = 0.f, den = 0.f;
-        for (int c = c0; c <= c1; ++c) {
-            const int slot = tile0 <= range_begin(p.total, p.ctas, c) ? 0 : 1;
-            const float* x = a.part + ((static_cast<int64_t>(c) * 2 + slot) * G + h) * (2 + kD);
-            const float m = ld_cg(x);
-            const float w = m == -INFINITY ? 0.f : exp2f(m - M);
-            num = fmaf(w, ld_cg(x + 2 + d), num);
-            den = fmaf(w, ld_cg(x + 1), den);
+        const int m = min(32, c1 - cb + 1);
+#pragma unroll 2
+        for (int x = warp; x < m; x += kWarps) {
+            const float4* src =
+                reinterpret_cast<const float4*>(a.part + part_slot(p, cb + x, tile0) * G * kD) + lane;
+#pragma unroll
+            for (int h = 0; h < G; ++h) {
+                const float4 v = __ldcg(src + h * 32);
+                const float f = __shfl_sync(0xffffffffu, w[h], x);
+                acc[h].x = fmaf(f, v.x, acc[h].x);
+                acc[h].y = fmaf(f, v.y, acc[h].y);
+                acc[h].z = fmaf(f, v.z, acc[h].z);
+                acc[h].w = fmaf(f, v.w, acc[h].w);
+            }
         }
-        a.out[(i * G + h) * kD + d] = den == 0.f ? 0.f : num / den;
-        if (a.lse && d == 0) a.lse[i * G + h] = lse_of(M, den);
+    }
+#pragma unroll
+    for (int h = 0; h < G; ++h) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) den[h] += __shfl_xor_sync(0xffffffffu, den[h], o);
+        if (warp > 0) reinterpret_cast<float4*>(red)[((warp - 1) * G + h) * 32 + lane] = acc[h];
+    }
+    named_sync(kBar, kWarps * 32);
+    if (warp > 0) return;
+#pragma unroll
+    for (int h = 0; h < G; ++h) {
+        float4 o = acc[h];
+#pragma unroll
+        for (int x = 0; x < kWarps - 1; ++x) {
+            const float4 v = reinterpret_cast<const float4*>(red)[(x * G + h) * 32 + lane];
+            o.x += v.x;
+            o.y += v.y;
+            o.z += v.z;
+            o.w += v.w;
+        }
+        const float d = den[h];
+        reinterpret_cast<float4*>(a.out + (i * G + h) * kD)[lane] =
+            d == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
+                     : make_float4(o.x / d, o.y / d, o.z / d, o.w / d);
+        if (a.lse && lane == 0) a.lse[i * G + h] = lse_of(M[h], d);
     }
 }
 
