@@ -553,13 +553,12 @@ PagedCache paged_cache(const int32_t* table, int64_t page_rows, int64_t pages_pe
 }
 
 struct DecodePagedWs {
-    size_t counters, zero_end, part, part_ml, total;
+    size_t counters, part, part_ml, total;
 };
 DecodePagedWs decode_paged_ws(int64_t n_units, int G) {
     DecodePagedWs w;
     Carve c;
     w.counters = c.take(static_cast<size_t>(n_units) * 4);
-    w.zero_end = c.off;
     const size_t slots = 2 * decode_paged_ctas(static_cast<int>(sm_count_or_default()));
     w.part = c.take(slots * G * kD * 4);
     w.part_ml = c.take(slots * G * 8);
@@ -1239,6 +1238,8 @@ tri_status tri_decode_attention_paged(const void* q, const void* k_pool, const v
     if (!aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(out) ||
         !aligned4(n_valid) || !aligned4(lse))
         return TRI_ERR_INVALID_ARG;
+    // Tiles of 32 rows of all units in 31 bits.
+    if (a.sl.n > INT32_MAX / ((pages_per_unit * page_rows + 31) / 32)) return TRI_ERR_UNSUPPORTED;
     const DecodePagedWs w = decode_paged_ws(a.sl.n, G);
     if (!ws || !aligned16(ws) || ws_bytes < w.total) return TRI_ERR_WORKSPACE;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -1262,7 +1263,6 @@ tri_status tri_decode_attention_paged(const void* q, const void* k_pool, const v
         TRI_TRY(make_key_map(&kmap, k_pool, dt, n_pages * page_rows, box));
         TRI_TRY(make_key_map(&vmap, v_pool, dt, n_pages * page_rows, box));
     }
-    TRI_CUDA(cudaMemsetAsync(ws, 0, w.zero_end, s));
     return cuda_status(box ? launch_decode_paged_tc(G, kmap, vmap, box, a, n_sm, s)
                            : launch_decode_paged_rows(dt, G, a, n_sm, s));
 }

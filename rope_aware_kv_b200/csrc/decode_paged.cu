@@ -21,6 +21,13 @@
 
 namespace tri {
 
+__global__ void __launch_bounds__(256) decode_clear_kernel(uint32_t* flag, uint32_t* counters, int64_t n) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int64_t i = blockIdx.x * 256ll + threadIdx.x;
+    if (i == 0) *flag = 0;
+    if (i < n) counters[i] = 0;
+}
+
 constexpr int kRowThreads = 256;
 constexpr int kRowWarps = kRowThreads / 32;
 constexpr int kRowTile = 32;    // keys a warp takes at a time
@@ -80,8 +87,9 @@ __global__ void __launch_bounds__(kRowThreads, 1) decode_paged_rows_kernel(const
     float* red = reinterpret_cast<float*>(smem + row_ring_bytes<T>());
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t cap = a.pc.per_unit * a.pc.rows;
-    write_empty_units(a, G);
     const SplitPlan p = plan_split<kRowThreads>(a, kRowTile, kRowWarps);
+    SplitUnit split[2];
+    int n_split = 0;
     // This lane's slice of the warp's ring: [kRing][kGroup][K, V] of 4 dims.
     T* mine = ring + (static_cast<int64_t>(warp) * kRing * kGroup * 2 * 32 + lane) * 4;
     auto cell = [&](int slot, int key, int kv) {
@@ -90,11 +98,11 @@ __global__ void __launch_bounds__(kRowThreads, 1) decode_paged_rows_kernel(const
     const T* kp = static_cast<const T*>(a.k) + lane * 4;
     const T* vp = static_cast<const T*>(a.v) + lane * 4;
 
-    int64_t t = p.begin, i = p.unit, tile0 = p.tile0;
+    uint32_t t = p.begin, i = p.unit, tile0 = p.tile0;
     while (t < p.end) {
         const int64_t u = slice_unit(a.sl, i);
         const int64_t n = clamp_nvalid(a.n_valid, u, cap, nullptr);
-        const int64_t n_tiles = (n + kRowTile - 1) / kRowTile;
+        const uint32_t n_tiles = static_cast<uint32_t>(n + kRowTile - 1) / kRowTile;
         if (n_tiles == 0) {
             ++i;
             continue;
@@ -104,7 +112,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) decode_paged_rows_kernel(const
         float2 q[G][2], acc[G][2];
 #pragma unroll
         for (int h = 0; h < G; ++h) {
-            const T* qh = static_cast<const T*>(a.q) + (i * G + h) * kD + lane * 4;
+            const T* qh = static_cast<const T*>(a.q) + (static_cast<int64_t>(i) * G + h) * kD + lane * 4;
             load4(qh, q[h][0], q[h][1]);
             acc[h][0] = acc[h][1] = make_float2(0.f, 0.f);
         }
@@ -126,7 +134,10 @@ __global__ void __launch_bounds__(kRowThreads, 1) decode_paged_rows_kernel(const
                     row_next = -1;
                     if (j < n) {
                         row_next = paged_row(a.pc, u, j);
-                        if (row_next < 0) raise_flag(a.flag, TRI_FLAG_INDEX_RANGE);
+                        if (row_next < 0) {
+                            wait_for_clear();
+                            raise_flag(a.flag, TRI_FLAG_INDEX_RANGE);
+                        }
                     }
                 }
                 const int slot = static_cast<int>(g % kRing);
@@ -239,7 +250,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) decode_paged_rows_kernel(const
         }
         __syncthreads();
         const bool whole = b0 == 0 && b1 == n_tiles;
-        const int64_t slot = part_slot(p, blockIdx.x, tile0);
+        const uint32_t slot = part_slot(p, blockIdx.x, tile0);
         for (int e = tid; e < G * kD; e += kRowThreads) {
             const int h = e / kD, d = e % kD;
             float M = -INFINITY;
@@ -254,25 +265,38 @@ __global__ void __launch_bounds__(kRowThreads, 1) decode_paged_rows_kernel(const
                 den = fmaf(f, x[1], den);
             }
             if (whole) {
-                a.out[(i * G + h) * kD + d] = den == 0.f ? 0.f : num / den;
-                if (a.lse && d == 0) a.lse[i * G + h] = lse_of(M, den);
+                a.out[(static_cast<int64_t>(i) * G + h) * kD + d] = den == 0.f ? 0.f : num / den;
+                if (a.lse && d == 0) a.lse[static_cast<int64_t>(i) * G + h] = lse_of(M, den);
             } else {
                 a.part[(slot * G + h) * kD + d] = num;
                 if (d == 0) a.part_ml[slot * G + h] = make_float2(M, den);
             }
         }
-        if (!whole) join_split_unit<kRowWarps, 0, G>(a, p, i, tile0, n_tiles, red);
+        if (!whole) {
+            split[n_split].i = i;
+            split[n_split].tile0 = tile0;
+            split[n_split++].n_tiles = n_tiles;
+        }
         __syncthreads();  // red is rewritten by the next unit
         t = tile0 + b1;
         tile0 += n_tiles;
         ++i;
     }
+    join_split_units<kRowWarps, 0>(a, G, p, n_split, split);
+    write_empty_units(a, G);
 }
 
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
 int decode_paged_ctas(int n_sm) { return n_sm; }
+
+cudaError_t launch_decode_paged_clear(const DecodePagedArgs& a, cudaStream_t s) {
+    decode_clear_kernel<<<static_cast<unsigned>((a.sl.n + 255) / 256), 256, 0, s>>>(a.flag, a.counters,
+                                                                                   a.sl.n);
+    note_launch(s);
+    return cudaGetLastError();
+}
 
 template <typename T, int G>
 static cudaError_t launch_rows(const DecodePagedArgs& a, int n_sm, cudaStream_t s) {
@@ -281,9 +305,11 @@ static cudaError_t launch_rows(const DecodePagedArgs& a, int n_sm, cudaStream_t 
     cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(smem));
     if (e != cudaSuccess) return e;
-    fn<<<static_cast<unsigned>(decode_paged_ctas(n_sm)), kRowThreads, smem, s>>>(a);
-    note_launch(s);
-    return cudaGetLastError();
+    e = launch_decode_paged_clear(a, s);
+    if (e != cudaSuccess) return e;
+    e = launch_early(fn, decode_paged_ctas(n_sm), kRowThreads, smem, s, a);
+    if (e == cudaSuccess) note_launch(s);
+    return e;
 }
 
 template <typename T>

@@ -33,7 +33,6 @@ constexpr int kTcHalf = kTcTile * 128;     // 64 dims of the tile's rows: 16 KB
 constexpr int kTcMat = 2 * kTcHalf;        // K or V of a tile
 constexpr int kTcPRow = 64;                // bytes of a key's weights: 32 bf16
 
-// (q and p lie side by side: together they hold the joining of split units.)
 struct __align__(1024) TcShared {
     unsigned char k[kTcStages][kTcMat];
     unsigned char v[kTcStages][kTcMat];
@@ -155,32 +154,38 @@ decode_paged_tc_kernel(const __grid_constant__ CUtensorMap kmap,
         prefetch_tensormap(&vmap);
     }
     if (warp == 0) tc_alloc(&sm.tmem, 64);
-    write_empty_units(a, G);
+    // Columns 24 .. 31 of the weights stay zeros.
+    if (tid < kTcMath)
+        *reinterpret_cast<uint4*>(sm.p + tid * kTcPRow + ((3 ^ ((tid >> 1) & 3)) * 16)) =
+            make_uint4(0, 0, 0, 0);
     tc_fence_before();
     const SplitPlan p = plan_split<kTcThreads>(a, kTcTile, 1);  // (synchronises the CTA)
     tc_fence_after();
     const uint32_t tmem = sm.tmem;
 
     uint32_t it = 0;  // tiles of this CTA so far
-    int64_t t = p.begin, i = p.unit, tile0 = p.tile0;
+    uint32_t t = p.begin, i = p.unit, tile0 = p.tile0;
     if (warp == kTcMath / 32) {
         // ---- the loading warp: lane b brings box b ----
         const int n_boxes = kTcTile / box_rows;
         const uint64_t pol = policy_evict_first();
         for (; t < p.end; ++i) {
             const int64_t u = slice_unit(a.sl, i);
-            const int64_t n = clamp_nvalid(a.n_valid, u, cap, nullptr);
-            const int64_t n_tiles = (n + kTcTile - 1) / kTcTile;
+            const uint32_t n = clamp_nvalid(a.n_valid, u, cap, nullptr);
+            const uint32_t n_tiles = static_cast<uint32_t>(n + kTcTile - 1) / kTcTile;
             if (n_tiles == 0) continue;
-            const int64_t t1 = min(tile0 + n_tiles, p.end);
+            const uint32_t t1 = min(tile0 + n_tiles, p.end);
             for (; t < t1; ++t, ++it) {
                 const int stage = it % kTcStages;
                 const uint32_t parity = ((it / kTcStages) & 1) ^ 1;
-                const int64_t j = (t - tile0) * kTcTile + static_cast<int64_t>(lane) * box_rows;
+                const int64_t j = static_cast<int64_t>(t - tile0) * kTcTile + lane * box_rows;
                 int64_t row = -1;
                 if (lane < n_boxes && j < n) {
                     row = paged_row(a.pc, u, j);
-                    if (row < 0) raise_flag(a.flag, TRI_FLAG_INDEX_RANGE);
+                    if (row < 0) {
+                        wait_for_clear();
+                        raise_flag(a.flag, TRI_FLAG_INDEX_RANGE);
+                    }
                 }
                 const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, row >= 0)) * box_rows * 256;
                 const int off = lane * box_rows * 128;
@@ -216,16 +221,18 @@ decode_paged_tc_kernel(const __grid_constant__ CUtensorMap kmap,
         const uint32_t lanes = static_cast<uint32_t>(warp) * 32 << 16;  // this warp's TMEM lanes
         const uint32_t s_cols = tmem, o_cols = tmem + 32;
         const uint32_t page_rows = static_cast<uint32_t>(a.pc.rows);
+        SplitUnit split[2];
+        int n_split = 0;
         bool ok = true;
         while (t < p.end) {
             const int64_t u = slice_unit(a.sl, i);
-            const int64_t n = clamp_nvalid(a.n_valid, u, cap, nullptr);
-            const int64_t n_tiles = (n + kTcTile - 1) / kTcTile;
+            const uint32_t n = clamp_nvalid(a.n_valid, u, cap, nullptr);
+            const uint32_t n_tiles = static_cast<uint32_t>(n + kTcTile - 1) / kTcTile;
             if (n_tiles == 0) {
                 ++i;
                 continue;
             }
-            const int64_t t1 = min(tile0 + n_tiles, p.end);
+            const uint32_t t1 = min(tile0 + n_tiles, p.end);
             const bool from_start = t == tile0;
             // ---- Q, rows >= G zero; 16-byte chunk c of a 128-byte row r lies at c ^ (r & 7) ----
             for (int e = tid; e < 16 * 16; e += kTcMath) {
@@ -233,13 +240,10 @@ decode_paged_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                 uint4 x = make_uint4(0, 0, 0, 0);
                 if (r < G)
                     x = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
-                                                             (i * G + r) * kD) +
+                                                             (static_cast<int64_t>(i) * G + r) * kD) +
                               c);
                 *reinterpret_cast<uint4*>(sm.q[c >> 3] + r * 128 + ((c & 7) ^ (r & 7)) * 16) = x;
             }
-            // Columns 24 .. 31 of the weights are zeros.
-            *reinterpret_cast<uint4*>(sm.p + tid * kTcPRow + ((3 ^ ((tid >> 1) & 3)) * 16)) =
-                make_uint4(0, 0, 0, 0);
             float m[G], l[G], acc[G];
 #pragma unroll
             for (int h = 0; h < G; ++h) {
@@ -257,9 +261,9 @@ decode_paged_tc_kernel(const __grid_constant__ CUtensorMap kmap,
             };
             if (tid == 0) start_scores(it);
             // Whether this thread's key of tile x has a row (looked up a tile ahead).
-            auto has_row = [&](int64_t x) {
-                const int64_t j = (x - tile0) * kTcTile + tid;
-                return x < t1 && j < n && page_of(a.pc, u, static_cast<uint32_t>(j) / page_rows) >= 0;
+            auto has_row = [&](uint32_t x) {
+                const uint32_t j = (x - tile0) * kTcTile + tid;
+                return x < t1 && j < n && page_of(a.pc, u, j / page_rows) >= 0;
             };
             bool valid = has_row(t);
             for (; t < t1; ++t, ++it) {
@@ -372,27 +376,32 @@ decode_paged_tc_kernel(const __grid_constant__ CUtensorMap kmap,
             named_sync(1, kTcMath);
             if (*reinterpret_cast<volatile int*>(&sm.abort)) break;
             const bool whole = from_start && t1 == tile0 + n_tiles;
-            const int64_t slot = part_slot(p, blockIdx.x, tile0);
+            const uint32_t slot = part_slot(p, blockIdx.x, tile0);
 #pragma unroll
             for (int h = 0; h < G; ++h) {
                 const float den = (sm.wsum[0][h] + sm.wsum[1][h]) + (sm.wsum[2][h] + sm.wsum[3][h]);
                 if (whole) {
-                    a.out[(i * G + h) * kD + tid] = den == 0.f ? 0.f : acc[h] / den;
-                    if (a.lse && tid == 0) a.lse[i * G + h] = lse_of(m[h], den);
+                    a.out[(static_cast<int64_t>(i) * G + h) * kD + tid] = den == 0.f ? 0.f : acc[h] / den;
+                    if (a.lse && tid == 0) a.lse[static_cast<int64_t>(i) * G + h] = lse_of(m[h], den);
                 } else {
                     a.part[(slot * G + h) * kD + tid] = acc[h];
                     if (tid == 0) a.part_ml[slot * G + h] = make_float2(m[h], den);
                 }
             }
-            // (Q and P are free by now: every product of the unit is done.)
-            if (!whole)
-                join_split_unit<kTcMath / 32, 1, G>(a, p, i, tile0, n_tiles,
-                                                    reinterpret_cast<float*>(sm.q));
+            if (!whole) {
+                split[n_split].i = i;
+                split[n_split].tile0 = tile0;
+                split[n_split++].n_tiles = n_tiles;
+            }
             named_sync(1, kTcMath);  // wsum and Q are rewritten by the next unit
             tile0 += n_tiles;
             ++i;
         }
+        if (!*reinterpret_cast<volatile int*>(&sm.abort))
+            join_split_units<kTcMath / 32, 1>(a, G, p, n_split, split);
     }
+    wait_for_clear();
+    write_empty_units(a, G);
     tc_fence_before();
     __syncthreads();
     if (warp == 0) tc_dealloc(tmem, 64);
@@ -412,15 +421,15 @@ static cudaError_t launch_tc(const CUtensorMap& kmap, const CUtensorMap& vmap, i
                              const DecodePagedArgs& a, int n_sm, cudaStream_t s) {
     constexpr size_t smem = sizeof(TcShared) + 1024;
     static_assert(smem <= 227 * 1024, "tile ring too large");
-    static_assert(sizeof(TcShared::q) + sizeof(TcShared::p) >= (kTcMath / 32 - 1) * TRI_MAX_GROUP * kD * 4,
-                  "no room to join split units");
     auto* fn = decode_paged_tc_kernel<G>;
     cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(smem));
     if (e != cudaSuccess) return e;
-    fn<<<static_cast<unsigned>(decode_paged_ctas(n_sm)), kTcThreads, smem, s>>>(kmap, vmap, box_rows, a);
-    note_launch(s);
-    return cudaGetLastError();
+    e = launch_decode_paged_clear(a, s);
+    if (e != cudaSuccess) return e;
+    e = launch_early(fn, decode_paged_ctas(n_sm), kTcThreads, smem, s, kmap, vmap, box_rows, a);
+    if (e == cudaSuccess) note_launch(s);
+    return e;
 }
 
 cudaError_t launch_decode_paged_tc(int G, const CUtensorMap& kmap, const CUtensorMap& vmap,

@@ -41,7 +41,7 @@ struct DecodePagedArgs {
     float scale_log2;        // scale * log2(e)
     float* out;              // [sl.n][G][128]
     float* lse;              // [sl.n][G] or null
-    uint32_t* counters;      // [sl.n], zero on entry: segments of a unit that are done
+    uint32_t* counters;      // [sl.n]: segments of a unit that are done
     // Partial results of split units, two slots a CTA: accumulators
     // [2 * ctas][G][128] and (maximum, sum) [2 * ctas][G].
     float* part;
@@ -49,6 +49,9 @@ struct DecodePagedArgs {
     uint32_t* flag;
 };
 int decode_paged_ctas(int n_sm);
+// The first kernel of the call: clears the flag word and the counters while
+// the second one begins.
+cudaError_t launch_decode_paged_clear(const DecodePagedArgs& a, cudaStream_t s);
 // Any page size, both types.
 cudaError_t launch_decode_paged_rows(tri_dtype dt, int G, const DecodePagedArgs& a, int n_sm,
                                      cudaStream_t s);

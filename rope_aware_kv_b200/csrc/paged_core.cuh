@@ -8,9 +8,11 @@ namespace tri {
 
 // Cache unit of the call's i-th unit.
 __device__ __forceinline__ int64_t slice_unit(const UnitSlice& sl, int64_t i) {
+    // (counts of units, slots and rows fit 32 bits: cheaper divisions)
     if (sl.layer < 0) return i;
-    const int64_t seq = i / sl.n_kvheads, head = i - seq * sl.n_kvheads;
-    return (seq * sl.n_layers + sl.layer) * sl.n_kvheads + head;
+    const uint32_t heads = static_cast<uint32_t>(sl.n_kvheads);
+    const uint32_t seq = static_cast<uint32_t>(i) / heads, head = static_cast<uint32_t>(i) - seq * heads;
+    return (seq * sl.n_layers + sl.layer) * heads + head;
 }
 
 // Page of slot `slot` of unit u, or -1.
@@ -21,9 +23,10 @@ __device__ __forceinline__ int64_t page_of(const PagedCache& pc, int64_t u, int6
 
 // Physical row of row j of unit u, or -1 when its page is not in the pool.
 __device__ __forceinline__ int64_t paged_row(const PagedCache& pc, int64_t u, int64_t j) {
-    const int64_t slot = j / pc.rows;
+    const uint32_t rows = static_cast<uint32_t>(pc.rows);
+    const uint32_t slot = static_cast<uint32_t>(j) / rows;
     const int64_t pg = page_of(pc, u, slot);
-    return pg < 0 ? -1 : pg * pc.rows + (j - slot * pc.rows);
+    return pg < 0 ? -1 : pg * pc.rows + (static_cast<uint32_t>(j) - slot * rows);
 }
 
 // ---------------------------------------------------------------------------
@@ -33,66 +36,68 @@ __device__ __forceinline__ int64_t paged_row(const PagedCache& pc, int64_t u, in
 // lies in several ranges is joined by the CTA that finishes it last.
 // ---------------------------------------------------------------------------
 struct SplitPlan {
-    int64_t total;   // tiles of all units
-    int ctas;        // CTAs with a range
-    int64_t begin;   // this CTA's tiles
-    int64_t end;
-    int64_t unit;    // first unit of the range
-    int64_t tile0;   // its first tile
+    uint32_t share;   // tiles of a CTA; the first `longer` ones have one more
+    uint32_t longer;
+    uint32_t begin;   // this CTA's tiles
+    uint32_t end;
+    uint32_t unit;    // first unit of the range
+    uint32_t tile0;   // its first tile
 };
 
-__device__ __forceinline__ int64_t range_begin(int64_t total, int ctas, int c) {
-    return total * c / ctas;
+__device__ __forceinline__ uint32_t range_begin(const SplitPlan& p, uint32_t c) {
+    return c * p.share + min(c, p.longer);
 }
 // The CTA whose range holds tile t.
-__device__ __forceinline__ int cta_of_tile(int64_t total, int ctas, int64_t t) {
-    return static_cast<int>(((t + 1) * ctas - 1) / total);
+__device__ __forceinline__ uint32_t cta_of_tile(const SplitPlan& p, uint32_t t) {
+    const uint32_t edge = p.longer * (p.share + 1);
+    return t < edge ? t / (p.share + 1) : p.longer + (t - edge) / p.share;
 }
 
 // Computed by every thread of the CTA together (kThreads of them, a multiple
 // of 32): each sums the tiles of its share of the units, a block scan places
 // the shares, and the thread whose share holds the CTA's first tile finds its
 // unit.  At least `min_tiles` tiles a CTA, while the call has that many.
+// (The host has checked that the tiles of the call fit 31 bits.)
 template <int kThreads>
-__device__ SplitPlan plan_split(const DecodePagedArgs& a, int tile, int min_tiles) {
-    __shared__ int64_t warp_sum[kThreads / 32];
-    __shared__ int64_t found[2];
+__device__ SplitPlan plan_split(const DecodePagedArgs& a, int tile, uint32_t min_tiles) {
+    __shared__ uint32_t warp_sum[kThreads / 32];
+    __shared__ uint32_t found[2];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t cap = a.pc.per_unit * a.pc.rows;
-    const int64_t per = (a.sl.n + kThreads - 1) / kThreads;
-    const int64_t i0 = tid * per < a.sl.n ? tid * per : a.sl.n;
-    const int64_t i1 = i0 + per < a.sl.n ? i0 + per : a.sl.n;
-    uint32_t* flag = blockIdx.x == 0 ? a.flag : nullptr;
-    int64_t sum = 0;
-    for (int64_t i = i0; i < i1; ++i)
-        sum += (clamp_nvalid(a.n_valid, slice_unit(a.sl, i), cap, flag) + tile - 1) / tile;
-    int64_t incl = sum;
+    const uint32_t units = static_cast<uint32_t>(a.sl.n);
+    const uint32_t per = (units + kThreads - 1) / kThreads;
+    const uint32_t i0 = min(tid * per, units), i1 = min(i0 + per, units);
+    auto tiles = [&](uint32_t i) -> uint32_t {
+        return static_cast<uint32_t>(clamp_nvalid(a.n_valid, slice_unit(a.sl, i), cap, nullptr) + (tile - 1)) / tile;
+    };
+    uint32_t sum = 0;
+#pragma unroll 4
+    for (uint32_t i = i0; i < i1; ++i) sum += tiles(i);
+    uint32_t incl = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int64_t x = __shfl_up_sync(0xffffffffu, incl, o);
+        const uint32_t x = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += x;
     }
     if (lane == 31) warp_sum[warp] = incl;
-    if (tid == 0) found[0] = a.sl.n;
     __syncthreads();
-    int64_t before = incl - sum, total = 0;
+    uint32_t before = incl - sum, total = 0;
 #pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) {
         if (w < warp) before += warp_sum[w];
         total += warp_sum[w];
     }
     SplitPlan p;
-    p.total = total;
-    const int64_t want = (total + min_tiles - 1) / min_tiles;
-    p.ctas = static_cast<int>(want < gridDim.x ? want : gridDim.x);
-    const int c = blockIdx.x;
-    p.begin = c < p.ctas ? range_begin(total, p.ctas, c) : total;
-    p.end = c < p.ctas ? range_begin(total, p.ctas, c + 1) : total;
+    const uint32_t ctas = max(min((total + min_tiles - 1) / min_tiles, gridDim.x), 1u);
+    const uint32_t c = blockIdx.x;
+    p.share = total / ctas;
+    p.longer = total - p.share * ctas;
+    p.begin = c < ctas ? range_begin(p, c) : total;
+    p.end = c < ctas ? range_begin(p, c + 1) : total;
     if (p.begin < p.end && before <= p.begin && p.begin < before + sum) {
-        int64_t t = before;
-        for (int64_t i = i0; i < i1; ++i) {
-            const int64_t nt =
-                (clamp_nvalid(a.n_valid, slice_unit(a.sl, i), cap, nullptr) + tile - 1) / tile;
+        uint32_t t = before;
+        for (uint32_t i = i0; i < i1; ++i) {
+            const uint32_t nt = per == 1 ? sum : tiles(i);
             if (p.begin < t + nt) {
                 found[0] = i;
                 found[1] = t;
@@ -107,13 +112,36 @@ __device__ SplitPlan plan_split(const DecodePagedArgs& a, int tile, int min_tile
     return p;
 }
 
-// Units without a row: zeros and an lse of -inf, spread over the grid.
+// The first kernel of the call clears the flag word and the counters and lets
+// the second one start at once; that one waits here before it touches them.
+__device__ __forceinline__ void wait_for_clear() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Launch a kernel that may start before the previous one of the stream has
+// ended (it waits with wait_for_clear).
+template <typename... P, typename... A>
+cudaError_t launch_early(void (*fn)(P...), unsigned grid, unsigned threads, size_t smem, cudaStream_t s,
+                         const A&... args) {
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, fn, args...);
+}
+
+// Units without a row: zeros and an lse of -inf, spread over the grid; counts
+// out of range are flagged.  (After wait_for_clear.)
 __device__ __forceinline__ void write_empty_units(const DecodePagedArgs& a, int G) {
     const int64_t cap = a.pc.per_unit * a.pc.rows;
     const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
     for (int64_t i = blockIdx.x + static_cast<int64_t>(gridDim.x) * threadIdx.x; i < a.sl.n;
          i += step) {
-        if (clamp_nvalid(a.n_valid, slice_unit(a.sl, i), cap, nullptr) > 0) continue;
+        if (clamp_nvalid(a.n_valid, slice_unit(a.sl, i), cap, a.flag) > 0) continue;
         float4* o = reinterpret_cast<float4*>(a.out + i * G * kD);
         for (int e = 0; e < G * kD / 4; ++e) o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (a.lse)
@@ -129,98 +157,96 @@ __device__ __forceinline__ float lse_of(float m, float l) {
 
 // Partial result of a unit's segment: slot 2 c of CTA c, or 2 c + 1 for a unit
 // that begins inside the CTA's range.
-__device__ __forceinline__ int64_t part_slot(const SplitPlan& p, int c, int64_t tile0) {
-    return 2 * static_cast<int64_t>(c) + (tile0 <= range_begin(p.total, p.ctas, c) ? 0 : 1);
+__device__ __forceinline__ uint32_t part_slot(const SplitPlan& p, uint32_t c, uint32_t tile0) {
+    return 2 * c + (tile0 <= range_begin(p, c) ? 0 : 1);
 }
 
-// This CTA's partial of unit i (first tile tile0, n_tiles tiles) is written;
-// the CTA that arrives last joins the unit's partials in CTA order,
+// A CTA's range holds at most two units that lie in other ranges too: its
+// first and its last.
+struct SplitUnit {
+    uint32_t i, tile0, n_tiles;
+};
+
+// The partials of this CTA's n_split split units are written; of each unit the
+// CTA that arrives last joins the partials in CTA order,
 //   out = sum_c 2^(m_c - M) acc_c / sum_c 2^(m_c - M) l_c.
-// Called by the kWarps * 32 threads of named barrier kBar.  A lane has 4 dims
-// of every head; the warps take the CTAs in turn, so the loads of a warp are
-// independent of one another, and are joined in warp order through red
-// ((kWarps - 1) * G * 128 floats of shared memory).
-template <int kWarps, int kBar, int G>
-__device__ void join_split_unit(const DecodePagedArgs& a, const SplitPlan& p, int64_t i,
-                                int64_t tile0, int64_t n_tiles, float* red) {
-    __shared__ bool last;
+// Called once, at the end, by the kWarps * 32 threads of named barrier kBar,
+// so the fence and the atomics are paid once.  A warp takes a head: lane c
+// holds the maximum and sum of the c-th of 32 CTAs, and every lane 4 dims of
+// the accumulators, kAhead of which are requested at a time.  The code is
+// short on purpose: it runs once per CTA, from a cold instruction cache, and
+// unrolled over the heads it took 7 us instead of 3.
+template <int kWarps, int kBar>
+__device__ void join_split_units(const DecodePagedArgs& a, int G, const SplitPlan& p, int n_split,
+                                 const SplitUnit (&split)[2]) {
+    constexpr int kAhead = 16;
+    __shared__ bool last[2];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int c0 = cta_of_tile(p.total, p.ctas, tile0);
-    const int c1 = cta_of_tile(p.total, p.ctas, tile0 + n_tiles - 1);
-    __threadfence();
+    wait_for_clear();
     named_sync(kBar, kWarps * 32);
-    if (tid == 0) last = atomicAdd(a.counters + i, 1u) == static_cast<uint32_t>(c1 - c0);
+    if (tid < n_split) {
+        const SplitUnit& s = split[tid];
+        const uint32_t more = cta_of_tile(p, s.tile0 + s.n_tiles - 1) - cta_of_tile(p, s.tile0);
+        __threadfence();
+        last[tid] = atomicAdd(a.counters + s.i, 1u) == more;
+        __threadfence();
+    }
     named_sync(kBar, kWarps * 32);
-    if (!last) return;
-    __threadfence();
-    float M[G], den[G];
-    float4 acc[G];
+#pragma unroll 1
+    for (int q = warp; q < n_split * G; q += kWarps) {
+        const int which = q >= G, h = which ? q - G : q;
+        if (!last[which]) continue;
+        const uint32_t tile0 = split[which].tile0;
+        const int64_t i = split[which].i;
+        const int c0 = cta_of_tile(p, tile0), c1 = cta_of_tile(p, tile0 + split[which].n_tiles - 1);
+        // The unit's slots: slot0 of c0, then 2 c.
+        const uint32_t slot0 = part_slot(p, c0, tile0);
+        auto slot = [&](int c) { return (c == c0 ? slot0 : 2 * c) * G + h; };
+        float M = -INFINITY, den = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+        for (int cb = c0; cb <= c1; cb += 32) {
+            const int n = min(32, c1 - cb + 1);
+            const float2 x = __ldcg(a.part_ml + slot(cb + min(lane, n - 1)));
+            float4 v[kAhead];
 #pragma unroll
-    for (int h = 0; h < G; ++h) {
-        M[h] = -INFINITY;
-        den[h] = 0.f;
-        acc[h] = make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-    for (int c = c0 + lane; c <= c1; c += 32) {
-        const float2* ml = a.part_ml + part_slot(p, c, tile0) * G;
+            for (int r = 0; r < kAhead; ++r)
+                v[r] = __ldcg(reinterpret_cast<const float4*>(a.part + slot(cb + min(r, n - 1)) * kD) + lane);
+            float m = x.x;
 #pragma unroll
-        for (int h = 0; h < G; ++h) M[h] = fmaxf(M[h], __ldcg(ml + h).x);
-    }
+            for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            m = fmaxf(m, M);
+            const float base = m == -INFINITY ? 0.f : m;
+            const float f = exp2f(M - base);
+            const float w = lane < n ? exp2f(x.x - base) : 0.f;
+            float l = lane < n ? w * x.y : 0.f;
 #pragma unroll
-    for (int h = 0; h < G; ++h) {
+            for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+            M = m;
+            den = fmaf(den, f, l);
+            acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+#pragma unroll 1
+            for (int b = 0; b < n; b += kAhead) {
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) M[h] = fmaxf(M[h], __shfl_xor_sync(0xffffffffu, M[h], o));
-    }
-    for (int cb = c0; cb <= c1; cb += 32) {
-        float w[G];
-        const bool in = cb + lane <= c1;
-        const float2* ml = a.part_ml + part_slot(p, in ? cb + lane : cb, tile0) * G;
+                for (int r = 0; r < kAhead; ++r) {
+                    const float g = __shfl_sync(0xffffffffu, w, b + r);  // 0 past the last CTA
+                    if (b + r >= n) continue;
+                    acc.x = fmaf(g, v[r].x, acc.x);
+                    acc.y = fmaf(g, v[r].y, acc.y);
+                    acc.z = fmaf(g, v[r].z, acc.z);
+                    acc.w = fmaf(g, v[r].w, acc.w);
+                }
+                if (b + kAhead >= n) break;
 #pragma unroll
-        for (int h = 0; h < G; ++h) {
-            const float2 x = __ldcg(ml + h);
-            w[h] = in && x.x != -INFINITY ? exp2f(x.x - M[h]) : 0.f;
-            if (in) den[h] = fmaf(w[h], x.y, den[h]);
-        }
-        const int m = min(32, c1 - cb + 1);
-#pragma unroll 2
-        for (int x = warp; x < m; x += kWarps) {
-            const float4* src =
-                reinterpret_cast<const float4*>(a.part + part_slot(p, cb + x, tile0) * G * kD) + lane;
-#pragma unroll
-            for (int h = 0; h < G; ++h) {
-                const float4 v = __ldcg(src + h * 32);
-                const float f = __shfl_sync(0xffffffffu, w[h], x);
-                acc[h].x = fmaf(f, v.x, acc[h].x);
-                acc[h].y = fmaf(f, v.y, acc[h].y);
-                acc[h].z = fmaf(f, v.z, acc[h].z);
-                acc[h].w = fmaf(f, v.w, acc[h].w);
+                for (int r = 0; r < kAhead; ++r)
+                    v[r] = __ldcg(reinterpret_cast<const float4*>(
+                                      a.part + slot(cb + min(b + kAhead + r, n - 1)) * kD) + lane);
             }
         }
-    }
-#pragma unroll
-    for (int h = 0; h < G; ++h) {
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) den[h] += __shfl_xor_sync(0xffffffffu, den[h], o);
-        if (warp > 0) reinterpret_cast<float4*>(red)[((warp - 1) * G + h) * 32 + lane] = acc[h];
-    }
-    named_sync(kBar, kWarps * 32);
-    if (warp > 0) return;
-#pragma unroll
-    for (int h = 0; h < G; ++h) {
-        float4 o = acc[h];
-#pragma unroll
-        for (int x = 0; x < kWarps - 1; ++x) {
-            const float4 v = reinterpret_cast<const float4*>(red)[(x * G + h) * 32 + lane];
-            o.x += v.x;
-            o.y += v.y;
-            o.z += v.z;
-            o.w += v.w;
-        }
-        const float d = den[h];
         reinterpret_cast<float4*>(a.out + (i * G + h) * kD)[lane] =
-            d == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
-                     : make_float4(o.x / d, o.y / d, o.z / d, o.w / d);
-        if (a.lse && lane == 0) a.lse[i * G + h] = lse_of(M[h], d);
+            den == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
+                       : make_float4(acc.x / den, acc.y / den, acc.z / den, acc.w / den);
+        if (a.lse && lane == 0) a.lse[i * G + h] = lse_of(M, den);
     }
 }
 
