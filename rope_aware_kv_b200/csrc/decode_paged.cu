@@ -88,7 +88,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) decode_paged_rows_kernel(const
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t cap = a.pc.per_unit * a.pc.rows;
     const SplitPlan p = plan_split<kRowThreads>(a, kRowTile, kRowWarps);
-    SplitUnit split[2];
+    SplitUnit split[2] = {};
     int n_split = 0;
     // This lane's slice of the warp's ring: [kRing][kGroup][K, V] of 4 dims.
     T* mine = ring + (static_cast<int64_t>(warp) * kRing * kGroup * 2 * 32 + lane) * 4;
@@ -273,9 +273,9 @@ __global__ void __launch_bounds__(kRowThreads, 1) decode_paged_rows_kernel(const
             }
         }
         if (!whole) {
-            split[n_split].i = i;
-            split[n_split].tile0 = tile0;
-            split[n_split++].n_tiles = n_tiles;
+            split[0] = n_split ? split[0] : SplitUnit{i, tile0, n_tiles, false};
+            split[1] = SplitUnit{i, tile0, n_tiles, false};
+            ++n_split;
         }
         __syncthreads();  // red is rewritten by the next unit
         t = tile0 + b1;

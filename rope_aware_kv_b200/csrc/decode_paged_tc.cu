@@ -179,14 +179,12 @@ decode_paged_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                 const int stage = it % kTcStages;
                 const uint32_t parity = ((it / kTcStages) & 1) ^ 1;
                 const int64_t j = static_cast<int64_t>(t - tile0) * kTcTile + lane * box_rows;
-                int64_t row = -1;
-                if (lane < n_boxes && j < n) {
-                    row = paged_row(a.pc, u, j);
-                    if (row < 0) {
-                        wait_for_clear();
-                        raise_flag(a.flag, TRI_FLAG_INDEX_RANGE);
-                    }
+                int64_t row = lane < n_boxes && j < cap ? paged_row(a.pc, u, j) : -1;
+                if (lane < n_boxes && j < n && row < 0) {
+                    wait_for_clear();
+                    raise_flag(a.flag, TRI_FLAG_INDEX_RANGE);
                 }
+                if (j >= n) row = -1;
                 const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, row >= 0)) * box_rows * 256;
                 const int off = lane * box_rows * 128;
                 bool ok = mbar_wait(&sm.k_empty[stage], parity, a.flag);
@@ -221,7 +219,7 @@ decode_paged_tc_kernel(const __grid_constant__ CUtensorMap kmap,
         const uint32_t lanes = static_cast<uint32_t>(warp) * 32 << 16;  // this warp's TMEM lanes
         const uint32_t s_cols = tmem, o_cols = tmem + 32;
         const uint32_t page_rows = static_cast<uint32_t>(a.pc.rows);
-        SplitUnit split[2];
+        SplitUnit split[2] = {};
         int n_split = 0;
         bool ok = true;
         while (t < p.end) {
@@ -389,9 +387,9 @@ decode_paged_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                 }
             }
             if (!whole) {
-                split[n_split].i = i;
-                split[n_split].tile0 = tile0;
-                split[n_split++].n_tiles = n_tiles;
+                split[0] = n_split ? split[0] : SplitUnit{i, tile0, n_tiles, false};
+                split[1] = SplitUnit{i, tile0, n_tiles, false};
+                ++n_split;
             }
             named_sync(1, kTcMath);  // wsum and Q are rewritten by the next unit
             tile0 += n_tiles;

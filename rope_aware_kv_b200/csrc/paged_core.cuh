@@ -165,88 +165,152 @@ __device__ __forceinline__ uint32_t part_slot(const SplitPlan& p, uint32_t c, ui
 // first and its last.
 struct SplitUnit {
     uint32_t i, tile0, n_tiles;
+    bool last;  // this CTA joins it
 };
+
+// The heads h0, h0 + step, ... (kHeads of them at most, below `heads`) of the
+// split units, joined by one warp: head q is head q % G of unit q / G.  Lane c
+// holds the maximum and sum of the c-th of 32 CTAs, every lane 4 dims of the
+// accumulators; the accumulators of kAhead CTAs of all kHeads are requested
+// at a time.
+template <int kHeads, int kAhead>
+__device__ void join_heads(const DecodePagedArgs& a, int G, const SplitPlan& p,
+                           const SplitUnit (&split)[2], int heads, int h0, int step) {
+    const int lane = threadIdx.x & 31;
+    struct Head {
+        uint32_t i, c0, n, slot0, h;  // n = 0: none
+    } hd[kHeads];
+    uint32_t most = 0;
+#pragma unroll
+    for (int r = 0; r < kHeads; ++r) {
+        const int q = h0 + r * step;
+        const SplitUnit& s = split[q >= G && q < heads ? 1 : 0];
+        hd[r].i = s.i;
+        hd[r].h = q >= G ? q - G : q;
+        hd[r].c0 = cta_of_tile(p, s.tile0);
+        hd[r].n = q < heads && s.last ? cta_of_tile(p, s.tile0 + s.n_tiles - 1) - hd[r].c0 + 1 : 0;
+        hd[r].slot0 = part_slot(p, hd[r].c0, s.tile0);
+        most = max(most, hd[r].n);
+    }
+    // Slot of the unit's x-th CTA; x past the last one repeats it.
+    auto slot = [&](const Head& d, uint32_t x) -> uint32_t {
+        x = min(x, d.n - 1);
+        return (x == 0 ? d.slot0 : 2 * (d.c0 + x)) * G + d.h;
+    };
+    float M[kHeads], den[kHeads];
+    float4 acc[kHeads];
+#pragma unroll
+    for (int r = 0; r < kHeads; ++r) {
+        M[r] = -INFINITY;
+        den[r] = 0.f;
+        acc[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll 1
+    for (uint32_t cb = 0; cb < most; cb += 32) {
+        float2 x[kHeads];
+        float w[kHeads];
+        float4 v[kHeads][kAhead];
+#pragma unroll
+        for (int r = 0; r < kHeads; ++r)
+            if (hd[r].n) x[r] = __ldcg(a.part_ml + slot(hd[r], cb + lane));
+        auto request = [&](uint32_t b) {
+#pragma unroll
+            for (int r = 0; r < kHeads; ++r)
+#pragma unroll
+                for (int y = 0; y < kAhead; ++y)
+                    if (hd[r].n)
+                        v[r][y] = __ldcg(reinterpret_cast<const float4*>(
+                                             a.part + static_cast<int64_t>(slot(hd[r], b + y)) * kD) + lane);
+        };
+        request(cb);
+#pragma unroll
+        for (int r = 0; r < kHeads; ++r) {
+            const bool in = cb + lane < hd[r].n;
+            float m = in ? x[r].x : -INFINITY;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            m = fmaxf(m, M[r]);
+            const float base = m == -INFINITY ? 0.f : m;
+            const float f = exp2f(M[r] - base);
+            w[r] = in ? exp2f(x[r].x - base) : 0.f;
+            float l = in ? w[r] * x[r].y : 0.f;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+            M[r] = m;
+            den[r] = fmaf(den[r], f, l);
+            acc[r] = make_float4(acc[r].x * f, acc[r].y * f, acc[r].z * f, acc[r].w * f);
+        }
+#pragma unroll 1
+        for (uint32_t b = 0; b < 32 && cb + b < most; b += kAhead) {
+#pragma unroll
+            for (int r = 0; r < kHeads; ++r) {
+#pragma unroll
+                for (int y = 0; y < kAhead; ++y) {
+                    const float g = __shfl_sync(0xffffffffu, w[r], b + y);
+                    if (cb + b + y >= hd[r].n) continue;
+                    acc[r].x = fmaf(g, v[r][y].x, acc[r].x);
+                    acc[r].y = fmaf(g, v[r][y].y, acc[r].y);
+                    acc[r].z = fmaf(g, v[r][y].z, acc[r].z);
+                    acc[r].w = fmaf(g, v[r][y].w, acc[r].w);
+                }
+            }
+            if (b + kAhead < 32 && cb + b + kAhead < most) request(cb + b + kAhead);
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < kHeads; ++r) {
+        if (!hd[r].n) continue;
+        const int64_t row = static_cast<int64_t>(hd[r].i) * G + hd[r].h;
+        const float d = den[r];
+        reinterpret_cast<float4*>(a.out + row * kD)[lane] =
+            d == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
+                     : make_float4(acc[r].x / d, acc[r].y / d, acc[r].z / d, acc[r].w / d);
+        if (a.lse && lane == 0) a.lse[row] = lse_of(M[r], d);
+    }
+}
 
 // The partials of this CTA's n_split split units are written; of each unit the
 // CTA that arrives last joins the partials in CTA order,
 //   out = sum_c 2^(m_c - M) acc_c / sum_c 2^(m_c - M) l_c.
 // Called once, at the end, by the kWarps * 32 threads of named barrier kBar,
-// so the fence and the atomics are paid once.  A warp takes a head: lane c
-// holds the maximum and sum of the c-th of 32 CTAs, and every lane 4 dims of
-// the accumulators, kAhead of which are requested at a time.  The code is
-// short on purpose: it runs once per CTA, from a cold instruction cache, and
-// unrolled over the heads it took 7 us instead of 3.
+// so the fence and the atomics are paid once.  What bounds it is the latency
+// of its loads: with many heads to join from few CTAs each a warp takes four
+// heads at a time, else two with more CTAs at a time.
 template <int kWarps, int kBar>
 __device__ void join_split_units(const DecodePagedArgs& a, int G, const SplitPlan& p, int n_split,
-                                 const SplitUnit (&split)[2]) {
-    constexpr int kAhead = 16;
+                                 SplitUnit (&split)[2]) {
     __shared__ bool last[2];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, warp = tid >> 5;
     wait_for_clear();
     named_sync(kBar, kWarps * 32);
-    if (tid < n_split) {
-        const SplitUnit& s = split[tid];
-        const uint32_t more = cta_of_tile(p, s.tile0 + s.n_tiles - 1) - cta_of_tile(p, s.tile0);
-        __threadfence();
-        last[tid] = atomicAdd(a.counters + s.i, 1u) == more;
-        __threadfence();
+    uint32_t most = 0;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        if (x >= n_split) break;
+        const uint32_t more =
+            cta_of_tile(p, split[x].tile0 + split[x].n_tiles - 1) - cta_of_tile(p, split[x].tile0);
+        most = max(most, more + 1);
+        if (tid == x * 32) {
+            __threadfence();
+            last[x] = atomicAdd(a.counters + split[x].i, 1u) == more;
+            __threadfence();
+        }
     }
     named_sync(kBar, kWarps * 32);
+    bool any = false;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        split[x].last = x < n_split && last[x];
+        any = any || split[x].last;
+    }
+    if (!any) return;
+    const int heads = n_split * G;
+    if (most <= 4) {
 #pragma unroll 1
-    for (int q = warp; q < n_split * G; q += kWarps) {
-        const int which = q >= G, h = which ? q - G : q;
-        if (!last[which]) continue;
-        const uint32_t tile0 = split[which].tile0;
-        const int64_t i = split[which].i;
-        const int c0 = cta_of_tile(p, tile0), c1 = cta_of_tile(p, tile0 + split[which].n_tiles - 1);
-        // The unit's slots: slot0 of c0, then 2 c.
-        const uint32_t slot0 = part_slot(p, c0, tile0);
-        auto slot = [&](int c) { return (c == c0 ? slot0 : 2 * c) * G + h; };
-        float M = -INFINITY, den = 0.f;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int q = warp; q < heads; q += 4 * kWarps) join_heads<4, 4>(a, G, p, split, heads, q, kWarps);
+    } else {
 #pragma unroll 1
-        for (int cb = c0; cb <= c1; cb += 32) {
-            const int n = min(32, c1 - cb + 1);
-            const float2 x = __ldcg(a.part_ml + slot(cb + min(lane, n - 1)));
-            float4 v[kAhead];
-#pragma unroll
-            for (int r = 0; r < kAhead; ++r)
-                v[r] = __ldcg(reinterpret_cast<const float4*>(a.part + slot(cb + min(r, n - 1)) * kD) + lane);
-            float m = x.x;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            m = fmaxf(m, M);
-            const float base = m == -INFINITY ? 0.f : m;
-            const float f = exp2f(M - base);
-            const float w = lane < n ? exp2f(x.x - base) : 0.f;
-            float l = lane < n ? w * x.y : 0.f;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-            M = m;
-            den = fmaf(den, f, l);
-            acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
-#pragma unroll 1
-            for (int b = 0; b < n; b += kAhead) {
-#pragma unroll
-                for (int r = 0; r < kAhead; ++r) {
-                    const float g = __shfl_sync(0xffffffffu, w, b + r);  // 0 past the last CTA
-                    if (b + r >= n) continue;
-                    acc.x = fmaf(g, v[r].x, acc.x);
-                    acc.y = fmaf(g, v[r].y, acc.y);
-                    acc.z = fmaf(g, v[r].z, acc.z);
-                    acc.w = fmaf(g, v[r].w, acc.w);
-                }
-                if (b + kAhead >= n) break;
-#pragma unroll
-                for (int r = 0; r < kAhead; ++r)
-                    v[r] = __ldcg(reinterpret_cast<const float4*>(
-                                      a.part + slot(cb + min(b + kAhead + r, n - 1)) * kD) + lane);
-            }
-        }
-        reinterpret_cast<float4*>(a.out + (i * G + h) * kD)[lane] =
-            den == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
-                       : make_float4(acc.x / den, acc.y / den, acc.z / den, acc.w / den);
-        if (a.lse && lane == 0) a.lse[i * G + h] = lse_of(M, den);
+        for (int q = warp; q < heads; q += 2 * kWarps) join_heads<2, 16>(a, G, p, split, heads, q, kWarps);
     }
 }
 
