@@ -565,74 +565,81 @@ def tri_append(k_cache, v_cache, pos_cache, n_seq: int, n_valid: torch.Tensor,
 
 class _PagedCall:
     """Shape, type and device checks of one paged call, and the device, stream
-    and workspace that it runs with."""
+    and workspace that it runs with.  (Written for few Python operations: a
+    small call is bound by its host side.)"""
+
+    __slots__ = ("index", "stream", "n_units", "per_unit", "n_pages", "page_rows", "d")
 
     def __init__(self, page_table: torch.Tensor, stream):
         if not page_table.is_cuda:
             raise ValueError("libtri takes CUDA tensors")
-        self.dev = page_table.device
+        self.index = page_table.get_device()
         self.stream = stream
-        self.n_units, self.per_unit = self.ints("page_table", page_table, 2).shape
+        if page_table.dtype != torch.int32 or page_table.dim() != 2 or not page_table.is_contiguous():
+            self.refuse("page_table", page_table, torch.int32, "of 2 dimensions")
+        self.n_units, self.per_unit = page_table.shape
 
-    def ints(self, name, t, dims=1, shape=None):
-        return self.check(name, t, torch.int32, dims, shape)
-
-    def check(self, name, t, dtype, dims, shape=None):
+    def check(self, name, t, dtype, shape):
+        """t (None passes) is a contiguous tensor of this type and shape on the
+        call's device; a shape entry of -1 takes any size."""
         if t is None:
-            return None
+            return
+        if (t.dtype != dtype or t.get_device() != self.index or not t.is_contiguous()
+                or (t.shape != shape and (t.dim() != len(shape) or any(
+                    y not in (-1, x) for x, y in zip(t.shape, shape))))):
+            self.refuse(name, t, dtype, shape)
+
+    def refuse(self, name, t, dtype, shape):
         if t.dtype != dtype:
             raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-        if t.dim() != dims or (shape is not None and tuple(t.shape) != tuple(shape)):
-            raise ValueError(f"{name} must have shape {shape or f'of {dims} dimensions'}, "
-                             f"got {tuple(t.shape)}")
-        if t.device != self.dev:
-            raise ValueError(f"{name} must be on {self.dev}, got {t.device}")
+        if t.get_device() != self.index:
+            raise ValueError(f"{name} must be on cuda:{self.index}, got {t.device}")
         if not t.is_contiguous():
-            raise ValueError("libtri takes contiguous tensors")
-        return t
+            raise ValueError(f"libtri takes contiguous tensors: {name}")
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
 
     def pools(self, k_pool, v_pool):
-        _dt(k_pool)
-        self.check("k_pool", k_pool, k_pool.dtype, 3)
-        self.check("v_pool", v_pool, k_pool.dtype, 3, k_pool.shape)
-        return k_pool.shape
+        if k_pool.dtype != torch.bfloat16:
+            _dt(k_pool)
+        self.check("k_pool", k_pool, k_pool.dtype, (-1, -1, -1))
+        if v_pool is not None:
+            self.check("v_pool", v_pool, k_pool.dtype, k_pool.shape)
+        self.n_pages, self.page_rows, self.d = k_pool.shape
 
-    def units(self, n_seq, n_layers, n_kvheads):
+    def units(self, n_seq, n_layers, n_kvheads, layer):
+        """Units of the call: all of them or one layer's."""
         if n_seq * n_layers * n_kvheads != self.n_units:
             raise ValueError(f"page_table has {self.n_units} units, not {n_seq} x {n_layers} x "
                              f"{n_kvheads}")
+        return self.n_units if layer < 0 else n_seq * n_kvheads
 
     def empty(self, shape, dtype):
-        with self.on_stream():
-            return torch.empty(shape, dtype=dtype, device=self.dev)
-
-    def on_stream(self):
-        """The call's stream as the current one: a buffer made under it is
-        not handed out again before the call is done with it."""
-        return torch.cuda.stream(self.stream)
+        """A buffer of the call's stream: it is not handed out again before the
+        call is done with it."""
+        if self.stream is None:
+            return torch.empty(shape, dtype=dtype, device=self.index)
+        with torch.cuda.stream(self.stream):
+            return torch.empty(shape, dtype=dtype, device=self.index)
 
     def run(self, name, nbytes, ws, args):
         if ws is None:
-            ws = self.empty(max(int(nbytes), 256), torch.uint8)
-        elif ws.device != self.dev or not ws.is_contiguous():
-            raise ValueError(f"ws must be a contiguous tensor on {self.dev}")
-        fn = getattr(load(), name)
-        args = (*args, ctypes.c_void_p(ws.data_ptr()), ws.numel() * ws.element_size())
-        if self.dev.index == torch.cuda.current_device():
-            s = self.stream if self.stream is not None else torch.cuda.current_stream()
-            _check(name, fn(*args, ctypes.c_void_p(s.cuda_stream)))
+            ws = self.empty(max(int(nbytes()), 256), torch.uint8)
+        elif ws.get_device() != self.index or not ws.is_contiguous():
+            raise ValueError(f"ws must be a contiguous tensor on cuda:{self.index}")
+        raw = (torch._C._cuda_getCurrentRawStream(self.index) if self.stream is None
+               else self.stream.cuda_stream)
+        fn = getattr(_lib or load(), name)
+        if self.index == torch.cuda.current_device():
+            code = fn(*args, ws.data_ptr(), ws.numel() * ws.element_size(), raw)
         else:
-            with torch.cuda.device(self.dev):
-                s = self.stream if self.stream is not None else torch.cuda.current_stream()
-                _check(name, fn(*args, ctypes.c_void_p(s.cuda_stream)))
+            with torch.cuda.device(self.index):
+                code = fn(*args, ws.data_ptr(), ws.numel() * ws.element_size(), raw)
+        if code:
+            raise TriError(name, code)
 
 
 def _p(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
-
-
-def _layer(layer: Optional[int]) -> int:
-    return -1 if layer is None else int(layer)
 
 
 def tri_decode_paged_workspace_bytes(n_units: int, G: int) -> int:
@@ -652,21 +659,23 @@ def tri_decode_attention_paged(q: torch.Tensor, k_pool: torch.Tensor, v_pool: to
     The units are all n_seq * n_layers * n_kvheads (``layer`` None or -1) or
     one layer's n_seq * n_kvheads; page_table and n_valid hold all of them."""
     c = _PagedCall(page_table, stream)
-    n_pages, page_rows, d = c.pools(k_pool, v_pool)
-    c.units(n_seq, n_layers, n_kvheads)
-    layer = _layer(layer)
-    U = n_seq * n_kvheads * (n_layers if layer < 0 else 1)
-    G = q.shape[1] if q.dim() == 3 else 0
-    c.check("q", q, k_pool.dtype, 3, (U, G, d))
-    c.ints("n_valid", n_valid, shape=(c.n_units,))
+    c.pools(k_pool, v_pool)
+    layer = -1 if layer is None else int(layer)
+    U = c.units(n_seq, n_layers, n_kvheads, layer)
+    d = c.d
+    c.check("q", q, k_pool.dtype, (U, -1, d))
+    G = q.shape[1]
+    c.check("n_valid", n_valid, torch.int32, (c.n_units,))
     if out is None:
         out = c.empty((U, G, d), torch.float32)
-    c.check("out", out, torch.float32, 3, (U, G, d))
-    c.check("lse", lse, torch.float32, 2, (U, G))
+    else:
+        c.check("out", out, torch.float32, (U, G, d))
+    c.check("lse", lse, torch.float32, (U, G))
     sc = (1.0 / d ** 0.5) if scale is None else float(scale)
-    c.run("tri_decode_attention_paged", 0 if ws is not None else tri_decode_paged_workspace_bytes(U, G),
-          ws, (_p(q), _p(k_pool), _p(v_pool), _dt(k_pool), n_seq, n_layers, n_kvheads, layer, G, d,
-               _p(page_table), page_rows, c.per_unit, n_pages, _p(n_valid), sc, _p(out), _p(lse)))
+    c.run("tri_decode_attention_paged", lambda: tri_decode_paged_workspace_bytes(U, G), ws,
+          (q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), _dt(k_pool), n_seq, n_layers,
+           n_kvheads, layer, G, d, page_table.data_ptr(), c.page_rows, c.per_unit, c.n_pages,
+           n_valid.data_ptr(), sc, out.data_ptr(), _p(lse)))
     return out
 
 
@@ -688,34 +697,29 @@ def tri_append_paged(k_pool: torch.Tensor, v_pool: Optional[torch.Tensor],
     there and unshared (``tri_pages_fit``); a unit that cannot take its rows is
     left as it is and sets a device flag."""
     c = _PagedCall(page_table, stream)
-    n_pages, page_rows, d = c.pools(k_pool, v_pool)
-    c.units(n_seq, n_layers, n_kvheads)
-    layer = _layer(layer)
-    U = n_seq * n_kvheads * (n_layers if layer < 0 else 1)
-    n_new = k_new.shape[1] if k_new.dim() == 3 else 0
-    c.check("k_new", k_new, k_pool.dtype, 3, (U, n_new, d))
-    c.check("v_new", v_new, k_pool.dtype, 3, (U, n_new, d))
-    c.ints("pos_new", pos_new, 2, (U, n_new))
-    c.ints("pos", pos, 2)
-    if pos is not None and pos.shape[0] != c.n_units:
-        raise ValueError(f"pos must have {c.n_units} rows, got {pos.shape[0]}")
-    cap = c.per_unit * page_rows if pos is None else pos.shape[1]
-    c.ints("n_valid", n_valid, shape=(c.n_units,))
-    c.ints("n_add", n_add, shape=(n_seq,))
-    c.ints("page_refs", page_refs, shape=(n_pages,))
-    c.check("p_cur", p_cur, torch.int64, 1, (n_seq,))
-    c.run("tri_append_paged", 0 if ws is not None else tri_append_paged_workspace_bytes(U), ws,
-          (_p(k_pool), _p(v_pool), _p(pos), _dt(k_pool), n_seq, n_layers, n_kvheads, layer, cap, d,
-           _p(page_table), page_rows, c.per_unit, n_pages, _p(page_refs), _p(n_valid), _p(p_cur),
-           _p(k_new), _p(v_new), _p(pos_new), _p(n_add), n_new))
+    c.pools(k_pool, v_pool)
+    layer = -1 if layer is None else int(layer)
+    U = c.units(n_seq, n_layers, n_kvheads, layer)
+    c.check("k_new", k_new, k_pool.dtype, (U, -1, c.d))
+    n_new = k_new.shape[1]
+    if v_new is not None:
+        c.check("v_new", v_new, k_pool.dtype, k_new.shape)
+    c.check("pos_new", pos_new, torch.int32, (U, n_new))
+    c.check("pos", pos, torch.int32, (c.n_units, -1))
+    cap = c.per_unit * c.page_rows if pos is None else pos.shape[1]
+    c.check("n_valid", n_valid, torch.int32, (c.n_units,))
+    c.check("n_add", n_add, torch.int32, (n_seq,))
+    c.check("page_refs", page_refs, torch.int32, (c.n_pages,))
+    c.check("p_cur", p_cur, torch.int64, (n_seq,))
+    c.run("tri_append_paged", lambda: tri_append_paged_workspace_bytes(U), ws,
+          (k_pool.data_ptr(), _p(v_pool), _p(pos), _dt(k_pool), n_seq, n_layers, n_kvheads, layer,
+           cap, c.d, page_table.data_ptr(), c.page_rows, c.per_unit, c.n_pages, _p(page_refs),
+           n_valid.data_ptr(), _p(p_cur), k_new.data_ptr(), _p(v_new), _p(pos_new), _p(n_add),
+           n_new))
 
 
 def tri_pages_workspace_bytes(n_units: int, pages_per_unit: int, n_pages: int) -> int:
     return load().tri_pages_workspace_bytes(n_units, pages_per_unit, n_pages)
-
-
-def _pages_ws_bytes(c: _PagedCall, n_pages: int, ws) -> int:
-    return 0 if ws is not None else tri_pages_workspace_bytes(c.n_units, c.per_unit, n_pages)
 
 
 def tri_pages_fit(k_pool: torch.Tensor, v_pool: Optional[torch.Tensor], page_table: torch.Tensor,
@@ -729,17 +733,19 @@ def tri_pages_fit(k_pool: torch.Tensor, v_pool: Optional[torch.Tensor], page_tab
     shared one) copied.  Returns ``n_free`` (int32 CUDA tensor [1]): the free
     pages left, or below 0 minus the pages lacking, when nothing was taken."""
     c = _PagedCall(page_table, stream)
-    n_pages, page_rows, d = c.pools(k_pool, v_pool)
-    c.ints("page_refs", page_refs, shape=(n_pages,))
-    c.ints("n_valid", n_valid, shape=(c.n_units,))
-    c.ints("n_add", n_add, shape=(n_seq,))
+    c.pools(k_pool, v_pool)
+    c.check("page_refs", page_refs, torch.int32, (c.n_pages,))
+    c.check("n_valid", n_valid, torch.int32, (c.n_units,))
+    c.check("n_add", n_add, torch.int32, (n_seq,))
     if n_free is None:
         n_free = c.empty((1,), torch.int32)
-    c.ints("n_free", n_free, shape=(1,))
-    c.run("tri_pages_fit", _pages_ws_bytes(c, n_pages, ws), ws,
-          (_p(k_pool), _p(v_pool), _dt(k_pool), n_seq, c.n_units, d, _p(page_table), page_rows,
-           c.per_unit, n_pages, _p(page_refs), _p(n_valid), _p(n_add), int(n_new), int(bool(own)),
-           _p(n_free)))
+    else:
+        c.check("n_free", n_free, torch.int32, (1,))
+    c.run("tri_pages_fit",
+          lambda: tri_pages_workspace_bytes(c.n_units, c.per_unit, c.n_pages), ws,
+          (k_pool.data_ptr(), _p(v_pool), _dt(k_pool), n_seq, c.n_units, c.d,
+           page_table.data_ptr(), c.page_rows, c.per_unit, c.n_pages, page_refs.data_ptr(),
+           n_valid.data_ptr(), _p(n_add), int(n_new), int(bool(own)), n_free.data_ptr()))
     return n_free
 
 
@@ -752,17 +758,17 @@ def tri_pages_fork(page_table: torch.Tensor, page_refs: torch.Tensor, page_rows:
     p_cur [n_seq] int64 follow.  Shared pages are copied by ``tri_pages_fit``
     when they are about to be written."""
     c = _PagedCall(page_table, stream)
-    n_pages = c.ints("page_refs", page_refs).shape[0]
-    c.ints("n_valid", n_valid, shape=(c.n_units,))
-    n_fork = c.ints("src_seq", src_seq).shape[0]
-    c.ints("dst_seq", dst_seq, shape=(n_fork,))
-    c.ints("pos", pos, 2)
-    if pos is not None and pos.shape[0] != c.n_units:
-        raise ValueError(f"pos must have {c.n_units} rows, got {pos.shape[0]}")
-    c.check("p_cur", p_cur, torch.int64, 1, (n_seq,))
-    c.run("tri_pages_fork", _pages_ws_bytes(c, n_pages, ws), ws,
-          (_p(page_table), int(page_rows), c.per_unit, n_pages, _p(page_refs), n_seq, c.n_units,
-           _p(src_seq), _p(dst_seq), n_fork, _p(n_valid), _p(pos),
+    c.check("page_refs", page_refs, torch.int32, (-1,))
+    n_pages = page_refs.shape[0]
+    c.check("n_valid", n_valid, torch.int32, (c.n_units,))
+    c.check("src_seq", src_seq, torch.int32, (-1,))
+    n_fork = src_seq.shape[0]
+    c.check("dst_seq", dst_seq, torch.int32, (n_fork,))
+    c.check("pos", pos, torch.int32, (c.n_units, -1))
+    c.check("p_cur", p_cur, torch.int64, (n_seq,))
+    c.run("tri_pages_fork", lambda: tri_pages_workspace_bytes(c.n_units, c.per_unit, n_pages), ws,
+          (page_table.data_ptr(), int(page_rows), c.per_unit, n_pages, page_refs.data_ptr(), n_seq,
+           c.n_units, src_seq.data_ptr(), dst_seq.data_ptr(), n_fork, n_valid.data_ptr(), _p(pos),
            0 if pos is None else pos.shape[1], _p(p_cur)))
 
 
@@ -774,14 +780,16 @@ def tri_pages_compact(k_pool: torch.Tensor, v_pool: Optional[torch.Tensor],
     them.  Returns ``n_live`` (int32 CUDA tensor [1]), the number of pages in
     use: those from there on are free."""
     c = _PagedCall(page_table, stream)
-    n_pages, page_rows, d = c.pools(k_pool, v_pool)
-    c.ints("page_refs", page_refs, shape=(n_pages,))
+    c.pools(k_pool, v_pool)
+    c.check("page_refs", page_refs, torch.int32, (c.n_pages,))
     if n_live is None:
         n_live = c.empty((1,), torch.int32)
-    c.ints("n_live", n_live, shape=(1,))
-    c.run("tri_pages_compact", _pages_ws_bytes(c, n_pages, ws), ws,
-          (_p(k_pool), _p(v_pool), _dt(k_pool), c.n_units, d, _p(page_table), page_rows, c.per_unit,
-           n_pages, _p(page_refs), _p(n_live)))
+    else:
+        c.check("n_live", n_live, torch.int32, (1,))
+    c.run("tri_pages_compact",
+          lambda: tri_pages_workspace_bytes(c.n_units, c.per_unit, c.n_pages), ws,
+          (k_pool.data_ptr(), _p(v_pool), _dt(k_pool), c.n_units, c.d, page_table.data_ptr(),
+           c.page_rows, c.per_unit, c.n_pages, page_refs.data_ptr(), n_live.data_ptr()))
     return n_live
 
 
