@@ -7,15 +7,20 @@
 // KV-compression objective: the softmax renormalised over the kept rows).
 //
 // rows kernel (any page size, both types).  Warps are independent: a warp
-// takes 32 keys at a time in groups of 4, its lanes holding 4 of the 128 dims
-// each.  Every lane copies its own 4 dims of the keys and values of the next
-// groups into a private shared-memory ring (cp.async, so no barrier is needed:
-// a lane reads back what it copied; a row without a page copies zeros).  The
-// 4 G partial dot products of a group are summed over the lanes by a
-// transposing butterfly (one shuffle per halved value instead of five per
-// value), which leaves one (key, head) score per lane for the online softmax;
-// the weights go back to all lanes by shuffle for the value product.  Scores,
-// running maxima, sums and accumulators are float32.
+// takes 32 keys at a time in groups of 8, copied row by row into its own
+// shared-memory ring (cp.async; a row without a page copies zeros).
+//   scores   8 lanes share a key, 16 of its dims each, interleaved by 16-byte
+//            chunks so that the lanes' reads fall on different banks; a lane
+//            has two keys of the group at a time, which halves the reads of
+//            Q.  The 8 lanes' partial sums of all heads are summed by a
+//            transposing butterfly (7 shuffles for 8 heads and 8 lanes, where
+//            32 lanes of 4 dims took 31), which leaves a lane the scores of
+//            one head for its keys and the online softmax.
+//   values   a lane has 4 dims; the weights come back through 256 bytes of
+//            shared memory as pairs of heads, so a packed FFMA2 multiplies
+//            two heads' weights with one dim.
+// Scores, running maxima, sums and accumulators are float32.  Bound by the
+// issue of its instructions, about 65 a key and warp at 8 heads.
 #include "paged_core.cuh"
 #include "tri_launch.h"
 
@@ -28,45 +33,38 @@ __global__ void __launch_bounds__(256) decode_clear_kernel(uint32_t* flag, uint3
     if (i < n) counters[i] = 0;
 }
 
-constexpr int kRowThreads = 256;
+constexpr int kRowThreads = 384;
 constexpr int kRowWarps = kRowThreads / 32;
 constexpr int kRowTile = 32;    // keys a warp takes at a time
-constexpr int kGroup = 4;       // keys whose scores are formed together
-constexpr int kRing = 6;        // groups in a warp's ring
+constexpr int kGroup = 8;       // keys whose scores are formed together
+constexpr int kRingBytes = 16384;  // of a warp: 2 groups of float32 rows, 4 of bf16
 
-constexpr int row_group_pad(int G) { return G <= 1 ? 1 : G <= 2 ? 2 : G <= 4 ? 4 : 8; }
+constexpr int row_heads_pad(int G) { return G <= 2 ? 2 : G <= 4 ? 4 : 8; }
 
-template <typename T>
-constexpr size_t row_ring_bytes() {
-    return static_cast<size_t>(kRowWarps) * kRing * kGroup * 2 * kD * sizeof(T);
-}
+// The results of the warps of one unit, which take the ring's place.
 template <int G>
 constexpr size_t row_red_bytes() {
     return static_cast<size_t>(kRowWarps) * G * (kD + 2) * sizeof(float);
 }
 
-// This lane's 4 dims of one row: global -> shared, zeros where the row has no
-// page.
-template <typename T>
-__device__ __forceinline__ void copy_lane(void* dst, const T* src, bool valid) {
-    constexpr int kBytes = 4 * sizeof(T);
-    const int n = valid ? kBytes : 0;
-    if constexpr (kBytes == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src),
-                     "r"(n)
-                     : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(smem_u32(dst)), "l"(src),
-                     "r"(n)
-                     : "memory");
-}
+struct RowShared {
+    float p[kRowWarps][kGroup * 8];  // weights [key][head]
+    float q[TRI_MAX_GROUP][kD];      // [head][piece][lane of 8][4 dims]
+    unsigned char ring[kRowWarps][kRingBytes];
+};
 
+__device__ __forceinline__ void copy16(void* dst, const void* src, bool valid) {
+    const int n = valid ? 16 : 0;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(n)
+                 : "memory");
+}
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void copy_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// 4 dims as two pairs.
 __device__ __forceinline__ void load4(const float* p, float2& a, float2& b) {
     const float4 x = *reinterpret_cast<const float4*>(p);
     a = make_float2(x.x, x.y);
@@ -80,171 +78,227 @@ __device__ __forceinline__ void load4(const __nv_bfloat16* p, float2& a, float2&
 
 template <typename T, int G>
 __global__ void __launch_bounds__(kRowThreads, 1) decode_paged_rows_kernel(const DecodePagedArgs a) {
-    constexpr int GP = row_group_pad(G);
-    constexpr int NV = kGroup * GP;  // values of a group's butterfly
+    constexpr int GP = row_heads_pad(G);     // heads of the butterfly
+    constexpr int HP = (G + 1) / 2;          // pairs of heads
+    constexpr int kRowBytes = kD * sizeof(T);
+    constexpr int kGroupBytes = kGroup * 2 * kRowBytes;  // [K, V][key][row]
+    constexpr int kRing = kRingBytes / kGroupBytes;
+    constexpr int kChunkDims = 16 / sizeof(T);           // dims of a 16-byte chunk
+    constexpr int kGroups = kRowTile / kGroup;
     extern __shared__ __align__(16) unsigned char smem[];
-    T* ring = reinterpret_cast<T*>(smem);
-    float* red = reinterpret_cast<float*>(smem + row_ring_bytes<T>());
+    RowShared& sm = *reinterpret_cast<RowShared*>(smem);
+    float* red = reinterpret_cast<float*>(sm.ring);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int sub = lane & 7, quad = lane >> 3;  // lane of a key, key of four
     const int64_t cap = a.pc.per_unit * a.pc.rows;
     const SplitPlan p = plan_split<kRowThreads>(a, kRowTile, kRowWarps);
     SplitUnit split[2] = {};
     int n_split = 0;
-    // This lane's slice of the warp's ring: [kRing][kGroup][K, V] of 4 dims.
-    T* mine = ring + (static_cast<int64_t>(warp) * kRing * kGroup * 2 * 32 + lane) * 4;
-    auto cell = [&](int slot, int key, int kv) {
-        return mine + ((slot * kGroup + key) * 2 + kv) * 32 * 4;
-    };
-    const T* kp = static_cast<const T*>(a.k) + lane * 4;
-    const T* vp = static_cast<const T*>(a.v) + lane * 4;
+    unsigned char* ring = sm.ring[warp];
+    float* pw = sm.p[warp];
+    const char* kp = static_cast<const char*>(a.k);
+    const char* vp = static_cast<const char*>(a.v);
 
     uint32_t t = p.begin, i = p.unit, tile0 = p.tile0;
     while (t < p.end) {
         const int64_t u = slice_unit(a.sl, i);
-        const int64_t n = clamp_nvalid(a.n_valid, u, cap, nullptr);
-        const uint32_t n_tiles = static_cast<uint32_t>(n + kRowTile - 1) / kRowTile;
+        const uint32_t n = clamp_nvalid(a.n_valid, u, cap, nullptr);
+        const uint32_t n_tiles = (n + kRowTile - 1) / kRowTile;
         if (n_tiles == 0) {
             ++i;
             continue;
         }
-        const int64_t b1 = min(n_tiles, p.end - tile0);  // tiles [t - tile0, b1) of the unit
-        const int64_t b0 = t - tile0;
-        float2 q[G][2], acc[G][2];
-#pragma unroll
-        for (int h = 0; h < G; ++h) {
-            const T* qh = static_cast<const T*>(a.q) + (static_cast<int64_t>(i) * G + h) * kD + lane * 4;
-            load4(qh, q[h][0], q[h][1]);
-            acc[h][0] = acc[h][1] = make_float2(0.f, 0.f);
+        const uint32_t b1 = min(n_tiles, p.end - tile0);  // tiles [b0, b1) of the unit
+        const uint32_t b0 = t - tile0;
+        // Q: piece r of lane s holds the 4 dims that it multiplies r-th.
+        for (int e = tid; e < G * (kD / 4); e += kRowThreads) {
+            const int h = e / (kD / 4), x = e % (kD / 4);  // dims 4 x ..
+            const int chunk = 4 * x / kChunkDims, part = x % (kChunkDims / 4);
+            const int r = (chunk >> 3) * (kChunkDims / 4) + part;
+            float2 lo, hi;
+            load4(static_cast<const T*>(a.q) + (static_cast<int64_t>(i) * G + h) * kD + 4 * x, lo, hi);
+            *reinterpret_cast<float4*>(&sm.q[h][(r * 8 + (chunk & 7)) * 4]) = make_float4(lo.x, lo.y, hi.x, hi.y);
         }
-        // This lane's score of a group: key lane / (32 / NV) / GP, head % GP.
-        const int vi = lane / (32 / NV);
-        const int my_key = vi / GP, my_head = vi % GP;
-        float m = -INFINITY, l = 0.f;  // of my_head; l over my_key's keys only
+        float2 acc[4][HP];  // [dim][pair of heads]
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+#pragma unroll
+            for (int h = 0; h < HP; ++h) acc[x][h] = make_float2(0.f, 0.f);
+        // This lane's head; its l is over its own keys.
+        const int my_head = sub / (8 / GP);
+        float m = -INFINITY, l = 0.f;
+        __syncthreads();
 
         // Tiles b0 + warp, b0 + warp + kRowWarps, ...; their groups in one
         // running order g = 0, 1, ... for the ring.
-        const int64_t mt = b1 - b0 > warp ? (b1 - b0 - warp + kRowWarps - 1) / kRowWarps : 0;
-        const int64_t n_groups = mt * (kRowTile / kGroup);
-        int64_t row_next = -1;  // physical row of this lane's key of the tile being loaded
-        auto issue = [&](int64_t g) {
+        const uint32_t mt = b1 - b0 > warp ? (b1 - b0 - warp + kRowWarps - 1) / kRowWarps : 0;
+        const uint32_t n_groups = mt * kGroups;
+        // Physical row of this lane's key of a tile (-1: none).  Looked up a
+        // tile before its first copy is issued.
+        auto look_up = [&](uint32_t tile) -> int32_t {
+            const uint32_t j = (b0 + warp + tile * kRowWarps) * kRowTile + lane;
+            if (tile >= mt || j >= n) return -1;
+            const int64_t r = paged_row(a.pc, u, j);
+            if (r < 0) {
+                wait_for_clear();
+                raise_flag(a.flag, TRI_FLAG_INDEX_RANGE);
+            }
+            return static_cast<int32_t>(r);
+        };
+        int32_t row_ahead = look_up(0), row_issue = -1;
+        uint32_t have = 0, have_issue = 0;  // keys with a row, of the tile used and the one issued
+        auto issue = [&](uint32_t g) {
             if (g < n_groups) {
-                const int gi = static_cast<int>(g % (kRowTile / kGroup));
+                const int gi = g % kGroups;
                 if (gi == 0) {
-                    const int64_t j = (b0 + warp + g / (kRowTile / kGroup) * kRowWarps) * kRowTile + lane;
-                    row_next = -1;
-                    if (j < n) {
-                        row_next = paged_row(a.pc, u, j);
-                        if (row_next < 0) {
-                            wait_for_clear();
-                            raise_flag(a.flag, TRI_FLAG_INDEX_RANGE);
-                        }
-                    }
+                    row_issue = row_ahead;
+                    have_issue = __ballot_sync(0xffffffffu, row_issue >= 0);
+                    row_ahead = look_up(g / kGroups + 1);
                 }
-                const int slot = static_cast<int>(g % kRing);
+                unsigned char* slot = ring + (g % kRing) * kGroupBytes;
+                constexpr int kLanes = kRowBytes / 16;  // of one row
 #pragma unroll
-                for (int key = 0; key < kGroup; ++key) {
-                    const int64_t r = __shfl_sync(0xffffffffu, row_next, gi * kGroup + key);
-                    const int64_t off = (r < 0 ? 0 : r) * kD;
-                    copy_lane(cell(slot, key, 0), kp + off, r >= 0);
-                    copy_lane(cell(slot, key, 1), vp + off, r >= 0);
+                for (int x = 0; x < kGroup; x += 32 / kLanes) {
+                    const int key = x + lane / kLanes, off = lane % kLanes * 16;
+                    const int32_t r = __shfl_sync(0xffffffffu, row_issue, gi * kGroup + key);
+                    const int64_t src = static_cast<int64_t>(r < 0 ? 0 : r) * kRowBytes + off;
+                    copy16(slot + key * kRowBytes + off, kp + src, r >= 0);
+                    copy16(slot + (kGroup + key) * kRowBytes + off, vp + src, r >= 0);
                 }
             }
             copy_commit();
         };
-        // Rows of the tile being used: looked up again rather than kept for
-        // the whole ring (the table entries are in L1).
-        int64_t row_now = -1;
-        for (int g = 0; g < kRing - 1; ++g) issue(g);
-        for (int64_t g = 0; g < n_groups; ++g) {
-            const int gi = static_cast<int>(g % (kRowTile / kGroup));
-            if (gi == 0) {
-                const int64_t j = (b0 + warp + g / (kRowTile / kGroup) * kRowWarps) * kRowTile + lane;
-                row_now = j < n ? paged_row(a.pc, u, j) : -1;
-            }
-            copy_wait<kRing - 2>();
-            const int slot = static_cast<int>(g % kRing);
-            // ---- partial dot products, then the transposing butterfly ----
-            float s[NV];
+        for (int g = 0; g < kRing; ++g) issue(g);
+        // (The ring is at most one tile ahead, so the tile in use is the one
+        // issued or the one before it.)
+        uint32_t have_next = have_issue;
+        static_assert(kRing <= kGroups, "ring longer than a tile");
+        for (uint32_t g = 0; g < n_groups; ++g) {
+            const int gi = g % kGroups;
+            if (gi == 0) have = have_next;
+            copy_wait<kRing - 1>();
+            __syncwarp();
+            const unsigned char* slot = ring + (g % kRing) * kGroupBytes;
+            // ---- partial dot products of keys quad and quad + 4 ----
+            float2 s0[G], s1[G];
 #pragma unroll
-            for (int key = 0; key < kGroup; ++key) {
-                float2 k0, k1;
-                load4(cell(slot, key, 0), k0, k1);
+            for (int h = 0; h < G; ++h) s0[h] = s1[h] = make_float2(0.f, 0.f);
+            const T* k0 = reinterpret_cast<const T*>(slot + quad * kRowBytes);
+            const T* k1 = reinterpret_cast<const T*>(slot + (quad + 4) * kRowBytes);
 #pragma unroll
-                for (int h = 0; h < GP; ++h) {
-                    if (h < G) {
-                        float2 d = __ffma2_rn(k0, q[h < G ? h : 0][0], make_float2(0.f, 0.f));
-                        d = __ffma2_rn(k1, q[h < G ? h : 0][1], d);
-                        s[key * GP + h] = d.x + d.y;
-                    } else {
-                        s[key * GP + h] = 0.f;
-                    }
+            for (int r = 0; r < 4; ++r) {
+                const int dim = (sub + 8 * (r / (kChunkDims / 4))) * kChunkDims + r % (kChunkDims / 4) * 4;
+                float2 x0, x1, y0, y1;
+                load4(k0 + dim, x0, x1);
+                load4(k1 + dim, y0, y1);
+#pragma unroll
+                for (int h = 0; h < G; ++h) {
+                    float2 q0, q1;
+                    load4(&sm.q[h][(r * 8 + sub) * 4], q0, q1);
+                    s0[h] = __ffma2_rn(x0, q0, s0[h]);
+                    s0[h] = __ffma2_rn(x1, q1, s0[h]);
+                    s1[h] = __ffma2_rn(y0, q0, s1[h]);
+                    s1[h] = __ffma2_rn(y1, q1, s1[h]);
                 }
             }
-            int o = 16;
+            // ---- the transposing butterfly over the key's 8 lanes ----
+            float sa[GP], sb[GP];
 #pragma unroll
-            for (int count = NV; count > 1; count >>= 1) {
-                const bool up = lane & o;
+            for (int h = 0; h < GP; ++h) {
+                sa[h] = h < G ? s0[h < G ? h : 0].x + s0[h < G ? h : 0].y : 0.f;
+                sb[h] = h < G ? s1[h < G ? h : 0].x + s1[h < G ? h : 0].y : 0.f;
+            }
+            int o = 4;
+#pragma unroll
+            for (int count = GP; count > 1; count >>= 1) {
+                const bool up = sub & o;
 #pragma unroll
                 for (int x = 0; x < count / 2; ++x) {
-                    const float keep = up ? s[x + count / 2] : s[x];
-                    const float give = up ? s[x] : s[x + count / 2];
-                    s[x] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+                    const float ka = up ? sa[x + count / 2] : sa[x], ga = up ? sa[x] : sa[x + count / 2];
+                    const float kb = up ? sb[x + count / 2] : sb[x], gb = up ? sb[x] : sb[x + count / 2];
+                    sa[x] = ka + __shfl_xor_sync(0xffffffffu, ga, o);
+                    sb[x] = kb + __shfl_xor_sync(0xffffffffu, gb, o);
                 }
                 o >>= 1;
             }
 #pragma unroll
-            for (; o > 0; o >>= 1) s[0] += __shfl_xor_sync(0xffffffffu, s[0], o);
-            const bool valid = __shfl_sync(0xffffffffu, row_now, gi * kGroup + my_key) >= 0;
-            const float sc = valid ? s[0] * a.scale_log2 : -INFINITY;
+            for (; o > 0; o >>= 1) {
+                sa[0] += __shfl_xor_sync(0xffffffffu, sa[0], o);
+                sb[0] += __shfl_xor_sync(0xffffffffu, sb[0], o);
+            }
             // ---- online softmax of my_head ----
-            float mx = sc;
-#pragma unroll
-            for (int x = GP * (32 / NV); x < 32; x <<= 1)
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+            const uint32_t bits = have >> (gi * kGroup + quad);
+            const bool va = bits & 1, vb = bits & 16;
+            const float xa = va ? sa[0] * a.scale_log2 : -INFINITY;
+            const float xb = vb ? sb[0] * a.scale_log2 : -INFINITY;
+            float mx = fmaxf(xa, xb);
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
             const float m_new = fmaxf(m, mx);
             const float base = m_new == -INFINITY ? 0.f : m_new;
-            const float pr = valid ? exp2f(sc - base) : 0.f;
+            const float wa = va ? exp2f(xa - base) : 0.f;
+            const float wb = vb ? exp2f(xb - base) : 0.f;
             if (__any_sync(0xffffffffu, m_new != m)) {
                 const float al = exp2f(m - base);
                 l *= al;
 #pragma unroll
-                for (int h = 0; h < G; ++h) {
-                    const float ah = __shfl_sync(0xffffffffu, al, h * (32 / NV));
-                    acc[h][0].x *= ah;
-                    acc[h][0].y *= ah;
-                    acc[h][1].x *= ah;
-                    acc[h][1].y *= ah;
+                for (int h = 0; h < HP; ++h) {
+                    const float a0 = __shfl_sync(0xffffffffu, al, 2 * h * (8 / GP));
+                    const float a1 = __shfl_sync(0xffffffffu, al, (2 * h + 1) * (8 / GP));
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        acc[x][h].x *= a0;
+                        acc[x][h].y *= a1;
+                    }
                 }
                 m = m_new;
             }
-            l += pr;
+            l += wa + wb;
+            if (sub % (8 / GP) == 0) {
+                pw[quad * GP + my_head] = wa;
+                pw[(quad + 4) * GP + my_head] = wb;
+            }
+            __syncwarp();
             // ---- values ----
 #pragma unroll
             for (int key = 0; key < kGroup; ++key) {
-                float2 v0, v1;
-                load4(cell(slot, key, 1), v0, v1);
+                float2 v01, v23;
+                load4(reinterpret_cast<const T*>(slot + (kGroup + key) * kRowBytes) + lane * 4, v01, v23);
+                float2 w[GP / 2];
 #pragma unroll
-                for (int h = 0; h < G; ++h) {
-                    const float w = __shfl_sync(0xffffffffu, pr, (key * GP + h) * (32 / NV));
-                    acc[h][0] = __ffma2_rn(make_float2(w, w), v0, acc[h][0]);
-                    acc[h][1] = __ffma2_rn(make_float2(w, w), v1, acc[h][1]);
+                for (int h = 0; h < GP / 2; h += 2) {
+                    if constexpr (GP >= 4)
+                        load4(pw + key * GP + 2 * h, w[h], w[h + 1 < GP / 2 ? h + 1 : h]);
+                    else
+                        w[h] = *reinterpret_cast<const float2*>(pw + key * GP);
+                }
+#pragma unroll
+                for (int h = 0; h < HP; ++h) {
+                    acc[0][h] = __ffma2_rn(w[h], make_float2(v01.x, v01.x), acc[0][h]);
+                    acc[1][h] = __ffma2_rn(w[h], make_float2(v01.y, v01.y), acc[1][h]);
+                    acc[2][h] = __ffma2_rn(w[h], make_float2(v23.x, v23.x), acc[2][h]);
+                    acc[3][h] = __ffma2_rn(w[h], make_float2(v23.y, v23.y), acc[3][h]);
                 }
             }
-            issue(g + kRing - 1);
+            __syncwarp();  // the group's slot and the weights are rewritten
+            issue(g + kRing);
+            if ((g + kRing) % kGroups == 0) have_next = have_issue;
         }
         copy_wait<0>();
         // ---- the warps' results, joined in warp order ----
-        // l of my_head: over the keys of a group (lanes GP * (32 / NV) apart).
-#pragma unroll
-        for (int x = GP * (32 / NV); x < 32; x <<= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
+        // l of my_head: over the keys' lanes.
+        l += __shfl_xor_sync(0xffffffffu, l, 8);
+        l += __shfl_xor_sync(0xffffffffu, l, 16);
+        __syncthreads();  // the rings are read; red takes their place
         float* rw = red + warp * G * (kD + 2);
 #pragma unroll
         for (int h = 0; h < G; ++h) {
             float2* d = reinterpret_cast<float2*>(rw + h * (kD + 2) + 2 + lane * 4);
-            d[0] = acc[h][0];
-            d[1] = acc[h][1];
+            const int x = h / 2;
+            d[0] = h & 1 ? make_float2(acc[0][x].y, acc[1][x].y) : make_float2(acc[0][x].x, acc[1][x].x);
+            d[1] = h & 1 ? make_float2(acc[2][x].y, acc[3][x].y) : make_float2(acc[2][x].x, acc[3][x].x);
         }
-        if (lane % (32 / NV) == 0 && my_key == 0 && my_head < G) {
+        if (quad == 0 && sub % (8 / GP) == 0 && my_head < G) {
             rw[my_head * (kD + 2)] = m;
             rw[my_head * (kD + 2) + 1] = l;
         }
@@ -268,7 +322,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) decode_paged_rows_kernel(const
                 a.out[(static_cast<int64_t>(i) * G + h) * kD + d] = den == 0.f ? 0.f : num / den;
                 if (a.lse && d == 0) a.lse[static_cast<int64_t>(i) * G + h] = lse_of(M, den);
             } else {
-                a.part[(slot * G + h) * kD + d] = num;
+                a.part[(static_cast<int64_t>(slot) * G + h) * kD + d] = num;
                 if (d == 0) a.part_ml[slot * G + h] = make_float2(M, den);
             }
         }
@@ -277,12 +331,12 @@ __global__ void __launch_bounds__(kRowThreads, 1) decode_paged_rows_kernel(const
             split[1] = SplitUnit{i, tile0, n_tiles, false};
             ++n_split;
         }
-        __syncthreads();  // red is rewritten by the next unit
+        __syncthreads();  // red and Q are rewritten by the next unit
         t = tile0 + b1;
         tile0 += n_tiles;
         ++i;
     }
-    join_split_units<kRowWarps, 0>(a, G, p, n_split, split);
+    join_split_units<kRowWarps, 0, 8>(a, G, p, n_split, split);
     write_empty_units(a, G);
 }
 
@@ -300,7 +354,8 @@ cudaError_t launch_decode_paged_clear(const DecodePagedArgs& a, cudaStream_t s) 
 
 template <typename T, int G>
 static cudaError_t launch_rows(const DecodePagedArgs& a, int n_sm, cudaStream_t s) {
-    constexpr size_t smem = row_ring_bytes<T>() + row_red_bytes<G>();
+    constexpr size_t smem = sizeof(RowShared);
+    static_assert(row_red_bytes<G>() <= sizeof(RowShared::ring) && smem <= 227 * 1024, "shared memory");
     auto* fn = decode_paged_rows_kernel<T, G>;
     cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(smem));

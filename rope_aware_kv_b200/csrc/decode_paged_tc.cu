@@ -396,7 +396,7 @@ decode_paged_tc_kernel(const __grid_constant__ CUtensorMap kmap,
             ++i;
         }
         if (!*reinterpret_cast<volatile int*>(&sm.abort))
-            join_split_units<kTcMath / 32, 1>(a, G, p, n_split, split);
+            join_split_units<kTcMath / 32, 1, 16>(a, G, p, n_split, split);
     }
     wait_for_clear();
     write_empty_units(a, G);

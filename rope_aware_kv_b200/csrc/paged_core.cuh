@@ -276,7 +276,8 @@ __device__ void join_heads(const DecodePagedArgs& a, int G, const SplitPlan& p,
 // so the fence and the atomics are paid once.  What bounds it is the latency
 // of its loads: with many heads to join from few CTAs each a warp takes four
 // heads at a time, else two with more CTAs at a time.
-template <int kWarps, int kBar>
+// (kAhead: as the kernel's registers allow.)
+template <int kWarps, int kBar, int kAhead>
 __device__ void join_split_units(const DecodePagedArgs& a, int G, const SplitPlan& p, int n_split,
                                  SplitUnit (&split)[2]) {
     __shared__ bool last[2];
@@ -310,7 +311,7 @@ __device__ void join_split_units(const DecodePagedArgs& a, int G, const SplitPla
         for (int q = warp; q < heads; q += 4 * kWarps) join_heads<4, 4>(a, G, p, split, heads, q, kWarps);
     } else {
 #pragma unroll 1
-        for (int q = warp; q < heads; q += 2 * kWarps) join_heads<2, 16>(a, G, p, split, heads, q, kWarps);
+        for (int q = warp; q < heads; q += 2 * kWarps) join_heads<2, kAhead>(a, G, p, split, heads, q, kWarps);
     }
 }
 
