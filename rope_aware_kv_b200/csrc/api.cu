@@ -567,7 +567,7 @@ DecodePagedWs decode_paged_ws(int64_t n_units, int G) {
 }
 
 struct PagesWs {
-    size_t writers, last, zero_end, slot_counts, page_counts, totals, list[4], total;
+    size_t writers, last, zero_end, counts, list[4], total;
 };
 PagesWs pages_ws(int64_t n_units, int64_t pages_per_unit, int64_t n_pages) {
     PagesWs w;
@@ -576,9 +576,7 @@ PagesWs pages_ws(int64_t n_units, int64_t pages_per_unit, int64_t n_pages) {
     w.writers = c.take(static_cast<size_t>(n_pages) * 4);
     w.last = c.take(static_cast<size_t>(n_pages) * 4);
     w.zero_end = c.off;
-    w.slot_counts = c.take(static_cast<size_t>((slots + kPageChunk - 1) / kPageChunk) * 8);
-    w.page_counts = c.take(static_cast<size_t>((n_pages + kPageChunk - 1) / kPageChunk) * 4);
-    w.totals = c.take(8);
+    w.counts = c.take(static_cast<size_t>(page_ctas(static_cast<int>(sm_count_or_default()))) * 16);
     const size_t most = static_cast<size_t>(slots < n_pages ? slots : n_pages);
     for (size_t& l : w.list) l = c.take(most * 4);
     w.total = c.off;
@@ -1359,13 +1357,12 @@ tri_status tri_pages_fit(void* k_pool, void* v_pool, tri_dtype dt, int64_t n_seq
     a.n_free = n_free;
     a.writers = reinterpret_cast<uint32_t*>(ws_at(ws, w.writers));
     a.last = reinterpret_cast<uint32_t*>(ws_at(ws, w.last));
-    a.slot_counts = reinterpret_cast<uint2*>(ws_at(ws, w.slot_counts));
-    a.page_counts = reinterpret_cast<uint32_t*>(ws_at(ws, w.page_counts));
+    a.counts = reinterpret_cast<uint4*>(ws_at(ws, w.counts));
     a.need_slot = reinterpret_cast<int32_t*>(ws_at(ws, w.list[0]));
     a.need_old = reinterpret_cast<int32_t*>(ws_at(ws, w.list[1]));
     a.copy_rank = reinterpret_cast<int32_t*>(ws_at(ws, w.list[2]));
     a.free_page = reinterpret_cast<int32_t*>(ws_at(ws, w.list[3]));
-    a.totals = reinterpret_cast<uint32_t*>(ws_at(ws, w.totals));
+    a.barrier = ws_flag(ws) + 1;
     a.flag = ws_flag(ws);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     TRI_CUDA(cudaMemsetAsync(ws, 0, w.zero_end, s));
@@ -1402,7 +1399,7 @@ tri_status tri_pages_fork(int32_t* page_table, int64_t page_rows, int64_t pages_
     a.n_fork = n_fork;
     a.done = ws_flag(ws) + 1;
     a.flag = ws_flag(ws);
-    return cuda_status(launch_pages_fork(a, s));
+    return cuda_status(launch_pages_fork(a, static_cast<int>(sm_count_or_default()), s));
 }
 
 tri_status tri_pages_compact(void* k_pool, void* v_pool, tri_dtype dt, int64_t n_units,
@@ -1424,13 +1421,13 @@ tri_status tri_pages_compact(void* k_pool, void* v_pool, tri_dtype dt, int64_t n
     a.pc = paged_cache(page_table, page_rows, pages_per_unit, n_pages, 1, n_units);
     a.refs = page_refs;
     a.n_live = n_live;
-    a.page_counts = reinterpret_cast<uint32_t*>(ws_at(ws, w.page_counts));
+    a.counts = reinterpret_cast<uint4*>(ws_at(ws, w.counts));
     // At most half of the pages move: both lists fit where tri_pages_fit
     // keeps its marks, and the ranks in its second half.
     a.from = reinterpret_cast<int32_t*>(ws_at(ws, w.writers));
     a.to = a.from + n_pages / 2;
     a.rank = reinterpret_cast<int32_t*>(ws_at(ws, w.last));
-    a.totals = reinterpret_cast<uint32_t*>(ws_at(ws, w.totals));
+    a.barrier = ws_flag(ws) + 1;
     a.flag = ws_flag(ws);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     TRI_CUDA(cudaMemsetAsync(ws, 0, kWsHeader, s));

@@ -86,7 +86,7 @@ struct AppendPagedArgs {
 };
 cudaError_t launch_append_paged(tri_dtype dt, const AppendPagedArgs& a, cudaStream_t s);
 
-constexpr int kPageChunk = 1024;  // slots or pages that one CTA counts and lists
+int page_ctas(int n_sm);  // CTAs of fit and compact
 
 struct FitArgs {
     void* k;
@@ -101,13 +101,12 @@ struct FitArgs {
     // scratch
     uint32_t* writers;        // [n_pages], zero on entry: slots of the page that will be written
     uint32_t* last;           // [n_pages], zero on entry: 1 + the last of them
-    uint2* slot_counts;       // [slot chunks]: pages asked for, of them copies
-    uint32_t* page_counts;    // [page chunks]: free pages
+    uint4* counts;            // [ctas]: pages asked for, of them copies, free pages
     int32_t* need_slot;       // [min(slots, pages)]: the i-th request's slot
     int32_t* need_old;        //   and the page it copies (-1: none)
     int32_t* copy_rank;       // [min(slots, pages)]: the requests that copy
     int32_t* free_page;       // [min(slots, pages)]: the i-th free page
-    uint32_t* totals;         // [2]: requests and copies that are served
+    uint32_t* barrier;        // zero on entry
     uint32_t* flag;
 };
 cudaError_t launch_pages_fit(tri_dtype dt, const FitArgs& a, int n_sm, cudaStream_t s);
@@ -127,7 +126,7 @@ struct ForkArgs {
     uint32_t* done;           // zero on entry: CTAs that are done
     uint32_t* flag;
 };
-cudaError_t launch_pages_fork(const ForkArgs& a, cudaStream_t s);
+cudaError_t launch_pages_fork(const ForkArgs& a, int n_sm, cudaStream_t s);
 
 struct CompactPagesArgs {
     void* k;
@@ -136,11 +135,11 @@ struct CompactPagesArgs {
     int32_t* refs;
     int32_t* n_live;          // or null
     // scratch
-    uint32_t* page_counts;    // [page chunks]: live pages
+    uint4* counts;            // [ctas]: live pages
     int32_t* from;            // [n_pages / 2]: the i-th page that moves
     int32_t* to;              //   and where it goes
     int32_t* rank;            // [n_pages]: i of a page that moves
-    uint32_t* totals;         // [2]: live pages, pages that move
+    uint32_t* barrier;        // zero on entry
     uint32_t* flag;
 };
 cudaError_t launch_pages_compact(tri_dtype dt, const CompactPagesArgs& a, int n_sm,

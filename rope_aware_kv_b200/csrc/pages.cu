@@ -88,35 +88,48 @@ __device__ void append_account(const AppendPagedArgs& a, int64_t i, const Append
                   static_cast<long long>(best) + 1);
 }
 
-// A warp copies new rows [x0, x1) of unit i, whose new rows begin at `first`:
-// half a warp moves a bf16 row (a whole one a float32 row) as 16-byte vectors.
+// A warp copies new rows [x0, x1) (at most 8) of unit i, whose new rows begin
+// at `first`: half a warp moves a bf16 row (a whole one a float32 row) as
+// 16-byte vectors, all rows of both arrays in flight before the first store.
+constexpr int kAppendFew = 8;
+
 template <int kVec>
 __device__ void append_rows(const AppendPagedArgs& a, int64_t i, int64_t u, int64_t first,
                             int64_t x0, int64_t x1, int lane) {
     constexpr int kPer = 32 / kVec;  // rows of one array in one instruction
-    uint4* k = static_cast<uint4*>(a.k);
-    uint4* v = static_cast<uint4*>(a.v);
+    constexpr int kIter = kAppendFew / kPer;
     const uint4* kn = static_cast<const uint4*>(a.k_new);
     const uint4* vn = static_cast<const uint4*>(a.v_new);
-    for (int64_t b = x0; b < x1; b += 32) {
-        const int64_t x = b + lane;
-        const int64_t row = x < x1 ? paged_row(a.pc, u, first + x) : 0;
-        if (a.pos && x < x1) a.pos[u * a.cap + first + x] = a.pos_new[i * a.n_new + x];
-        const int m = static_cast<int>(min(x1 - b, static_cast<int64_t>(32)));
-        for (int r = 0; r < m; r += kPer) {
-            const int mine = r + lane / kVec;
-            const int64_t dst = __shfl_sync(0xffffffffu, row, mine < m ? mine : 0);
-            if (mine < m && dst >= 0) {
-                const int64_t src = (i * a.n_new + b + mine) * kVec + lane % kVec;
-                k[dst * kVec + lane % kVec] = ld_stream(kn + src);
-                if (v) v[dst * kVec + lane % kVec] = ld_stream(vn + src);
-            }
+    const int64_t x = x0 + lane;
+    const int64_t row = x < x1 ? paged_row(a.pc, u, first + x) : -1;
+    if (a.pos && x < x1) a.pos[u * a.cap + first + x] = a.pos_new[i * a.n_new + x];
+    const int64_t src0 = (i * a.n_new + x0) * kVec;
+    const int m = static_cast<int>(x1 - x0) * kVec;
+    uint4 kv[kIter], vv[kIter];
+#pragma unroll
+    for (int r = 0; r < kIter; ++r) {
+        const int e = r * 32 + lane;
+        if (e < m) kv[r] = ld_stream(kn + src0 + e);
+    }
+    if (a.v) {
+#pragma unroll
+        for (int r = 0; r < kIter; ++r) {
+            const int e = r * 32 + lane;
+            if (e < m) vv[r] = ld_stream(vn + src0 + e);
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < kIter; ++r) {
+        const int64_t dst = __shfl_sync(0xffffffffu, row, r * kPer + lane / kVec);
+        const int e = r * 32 + lane;
+        if (e < m && dst >= 0) {
+            static_cast<uint4*>(a.k)[dst * kVec + lane % kVec] = kv[r];
+            if (a.v) static_cast<uint4*>(a.v)[dst * kVec + lane % kVec] = vv[r];
         }
     }
 }
 
 // Few new rows a unit: one warp does all of a unit.
-constexpr int kAppendFew = 8;
 
 template <int kVec>
 __global__ void __launch_bounds__(kThreads) append_few_kernel(const AppendPagedArgs a) {
@@ -151,8 +164,9 @@ __global__ void __launch_bounds__(kThreads) append_copy_kernel(const AppendPaged
     const int64_t u = slice_unit(a.sl, i);
     const int64_t add = rows_added(a.n_add, u / (a.pc.n_units / a.pc.n_seq), a.n_new, nullptr);
     constexpr int kRows = kAppendChunk / kWarps;
+    static_assert(kRows <= kAppendFew, "rows of a warp");
     const int64_t x0 = static_cast<int64_t>(blockIdx.x % chunks) * kAppendChunk + warp * kRows;
-    append_rows<kVec>(a, i, u, first, x0, min(x0 + kRows, add), lane);
+    if (x0 < add) append_rows<kVec>(a, i, u, first, x0, min(x0 + kRows, add), lane);
 }
 
 template <int kVec>
@@ -177,31 +191,68 @@ cudaError_t launch_append_paged(tri_dtype dt, const AppendPagedArgs& a, cudaStre
 }
 
 // ---------------------------------------------------------------------------
-// counting and listing by chunks
+// one grid, several phases (fit, compact)
 // ---------------------------------------------------------------------------
+// fit and compact are cooperative kernels: their phases (count, list, serve)
+// depend on one another over the whole pool, and a barrier of the grid costs
+// less than a launch.  CTA c of C owns the c-th C-th of the slots and of the
+// pages, so ranks over the pool are prefix sums of C counts.
+constexpr int kGridThreads = 512;
+constexpr int kGridWarps = kGridThreads / 32;
+
+// All CTAs of the grid have arrived (their writes are visible); `round` counts
+// the barriers.  Gives up after 2 s (TRI_FLAG_TIMEOUT): false, and the kernel
+// returns.
+__device__ bool grid_barrier(uint32_t* count, int round, uint32_t* flag) {
+    __shared__ bool ok;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        __threadfence();
+        atomicAdd(count, 1u);
+        const uint32_t want = static_cast<uint32_t>(round) * gridDim.x;
+        const uint64_t t0 = globaltimer_ns();
+        ok = true;
+        while (true) {
+            uint32_t now;
+            asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(now) : "l"(count) : "memory");
+            if (now >= want) break;
+            if (globaltimer_ns() - t0 > kWaitLimitNs) {
+                raise_flag(flag, TRI_FLAG_TIMEOUT);
+                ok = false;
+                break;
+            }
+        }
+    }
+    __syncthreads();
+    return ok;
+}
+
+// Part c of n things dealt to the CTAs of the grid.
+__device__ __forceinline__ int64_t part_begin(int64_t n, int64_t c) { return n * c / gridDim.x; }
+
 // Sum of `x` over the CTA, in every thread.
 __device__ __forceinline__ uint32_t cta_sum(uint32_t x) {
-    __shared__ uint32_t w[kWarps];
+    __shared__ uint32_t w[kGridWarps];
     x = __reduce_add_sync(0xffffffffu, x);
     __syncthreads();
     if ((threadIdx.x & 31) == 0) w[threadIdx.x >> 5] = x;
     __syncthreads();
     uint32_t t = 0;
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i) t += w[i];
+    for (int i = 0; i < kGridWarps; ++i) t += w[i];
     return t;
 }
 
 // Number of set `x` in the threads before this one, and of the whole CTA.
 __device__ __forceinline__ uint32_t cta_rank(bool x, uint32_t* total) {
-    __shared__ uint32_t w[kWarps];
+    __shared__ uint32_t w[kGridWarps];
     const uint32_t bal = __ballot_sync(0xffffffffu, x);
     __syncthreads();
     if ((threadIdx.x & 31) == 0) w[threadIdx.x >> 5] = __popc(bal);
     __syncthreads();
     uint32_t before = __popc(bal & ((1u << (threadIdx.x & 31)) - 1u)), t = 0;
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i) {
+    for (int i = 0; i < kGridWarps; ++i) {
         if (i < static_cast<int>(threadIdx.x >> 5)) before += w[i];
         t += w[i];
     }
@@ -209,15 +260,57 @@ __device__ __forceinline__ uint32_t cta_rank(bool x, uint32_t* total) {
     return before;
 }
 
-// Sums of counts[0 .. at) and counts[0 .. n), in every thread.
-__device__ __forceinline__ uint2 cta_prefix(const uint32_t* counts, int stride, int64_t n, int64_t at) {
-    uint32_t before = 0, all = 0;
-    for (int64_t i = threadIdx.x; i < n; i += kThreads) {
-        const uint32_t c = __ldcg(counts + i * stride);
-        all += c;
-        if (i < at) before += c;
+// Sums of the CTAs' counts x, y, z before CTA `at` and of all CTAs.
+struct PageSums {
+    uint32_t x, y, z, all_x, all_y, all_z;
+};
+__device__ __forceinline__ PageSums sum_counts(const uint4* counts, uint32_t at) {
+    PageSums s = {};
+    for (uint32_t c = threadIdx.x; c < gridDim.x; c += kGridThreads) {
+        const uint4 v = __ldcg(counts + c);
+        s.all_x += v.x;
+        s.all_y += v.y;
+        s.all_z += v.z;
+        if (c < at) {
+            s.x += v.x;
+            s.y += v.y;
+            s.z += v.z;
+        }
     }
-    return make_uint2(cta_sum(before), cta_sum(all));
+    s.x = cta_sum(s.x);
+    s.y = cta_sum(s.y);
+    s.z = cta_sum(s.z);
+    s.all_x = cta_sum(s.all_x);
+    s.all_y = cta_sum(s.all_y);
+    s.all_z = cta_sum(s.all_z);
+    return s;
+}
+
+// n 16-byte vectors, kLoads a thread in flight.
+constexpr int kLoads = 4;
+constexpr int kPiece = kLoads * kGridThreads;  // vectors that a CTA copies at a time: 32 KB
+
+__device__ __forceinline__ void copy_vectors(uint4* dst, const uint4* src, int64_t n) {
+    uint4 x[kLoads];
+#pragma unroll
+    for (int q = 0; q < kLoads; ++q) {
+        const int64_t e = q * kGridThreads + threadIdx.x;
+        if (e < n) x[q] = ld_stream(src + e);
+    }
+#pragma unroll
+    for (int q = 0; q < kLoads; ++q) {
+        const int64_t e = q * kGridThreads + threadIdx.x;
+        if (e < n) dst[e] = x[q];
+    }
+}
+
+template <typename Args>
+static cudaError_t launch_grid(void (*fn)(Args), const Args& a, int ctas, cudaStream_t s) {
+    void* args[1] = {const_cast<Args*>(&a)};
+    const cudaError_t e = cudaLaunchCooperativeKernel(reinterpret_cast<const void*>(fn), dim3(ctas),
+                                                      dim3(kGridThreads), args, 0, s);
+    if (e == cudaSuccess) note_launch(s);
+    return e;
 }
 
 // ---------------------------------------------------------------------------
@@ -234,7 +327,8 @@ __device__ __forceinline__ SlotWish slot_wish(const FitArgs& a, int64_t u, int64
                                               uint32_t* flag) {
     const int64_t cap = a.pc.per_unit * a.pc.rows;
     const int64_t n = clamp_nvalid(a.n_valid, u, cap, flag);
-    const int64_t add = rows_added(a.n_add, u / (a.pc.n_units / a.pc.n_seq), a.n_new, flag);
+    const uint32_t seq = static_cast<uint32_t>(u) / static_cast<uint32_t>(a.pc.n_units / a.pc.n_seq);
+    const int64_t add = rows_added(a.n_add, seq, a.n_new, flag);
     if (n + add > cap) raise_flag(flag, TRI_FLAG_NVALID_RANGE);
     SlotWish w;
     const int64_t row0 = slot * a.pc.rows;
@@ -245,14 +339,35 @@ __device__ __forceinline__ SlotWish slot_wish(const FitArgs& a, int64_t u, int64
     return w;
 }
 
-// Pages behind the last kept row are given back; pages that are shared and
-// will be written are marked.  A count that falls below 2 while this runs can
-// only make marks that the next kernel finds needless.
-__global__ void __launch_bounds__(kThreads) fit_mark_kernel(const FitArgs a) {
+// Whether the slot asks for a page (0: no, 1: it has none, 2: its page is
+// shared and it gets a copy).  Where every holder of a page writes it, the
+// last of them keeps it.
+__device__ __forceinline__ int slot_need(const FitArgs& a, int64_t id, int64_t* page) {
+    const uint32_t per = static_cast<uint32_t>(a.pc.per_unit);
+    const uint32_t u = static_cast<uint32_t>(id) / per, slot = static_cast<uint32_t>(id) - u * per;
+    const int64_t pg = __ldcg(a.pc.table + id);
+    const SlotWish w = slot_wish(a, u, slot, nullptr);
+    *page = pg;
+    if (!w.kept) return 0;
+    if (pg < 0) return 1;
+    const int32_t refs = __ldcg(a.refs + pg);
+    if (!w.written || refs <= 1) return 0;
+    return __ldcg(a.writers + pg) == static_cast<uint32_t>(refs) && __ldcg(a.last + pg) == id + 1 ? 0 : 2;
+}
+
+template <int kVec>
+__global__ void __launch_bounds__(kGridThreads, 2) pages_fit_kernel(const FitArgs a) {
+    const int tid = threadIdx.x;
+    const int64_t c = blockIdx.x;
     const int64_t slots = a.pc.n_units * a.pc.per_unit;
-    for (int64_t id = blockIdx.x * static_cast<int64_t>(kThreads) + threadIdx.x; id < slots;
-         id += static_cast<int64_t>(gridDim.x) * kThreads) {
-        const int64_t u = id / a.pc.per_unit, slot = id - u * a.pc.per_unit;
+    const uint32_t per = static_cast<uint32_t>(a.pc.per_unit);
+    const int64_t s0 = part_begin(slots, c), s1 = part_begin(slots, c + 1);
+    const int64_t p0 = part_begin(a.pc.n_pages, c), p1 = part_begin(a.pc.n_pages, c + 1);
+    // ---- pages behind the last kept row are given back; pages that are
+    // shared and will be written are marked.  (A count that falls below 2
+    // meanwhile only leaves a mark that nobody needs.) ----
+    for (int64_t id = s0 + tid; id < s1; id += kGridThreads) {
+        const uint32_t u = static_cast<uint32_t>(id) / per, slot = static_cast<uint32_t>(id) - u * per;
         const int64_t pg = a.pc.table[id];
         const SlotWish w = slot_wish(a, u, slot, slot == 0 ? a.flag : nullptr);
         if (pg < 0 || pg >= a.pc.n_pages) {
@@ -260,9 +375,7 @@ __global__ void __launch_bounds__(kThreads) fit_mark_kernel(const FitArgs a) {
                 raise_flag(a.flag, TRI_FLAG_INDEX_RANGE);
                 a.pc.table[id] = -1;
             }
-            continue;
-        }
-        if (!w.kept) {
+        } else if (!w.kept) {
             atomicSub(a.refs + pg, 1);
             a.pc.table[id] = -1;
         } else if (w.written && __ldcg(a.refs + pg) > 1) {
@@ -270,77 +383,35 @@ __global__ void __launch_bounds__(kThreads) fit_mark_kernel(const FitArgs a) {
             atomicMax(a.last + pg, static_cast<uint32_t>(id) + 1u);
         }
     }
-}
-
-// Whether the slot asks for a page (0: no, 1: it has none, 2: its page is
-// shared and it gets a copy).  Where every holder of a page writes it, the
-// last of them keeps it.
-__device__ __forceinline__ int slot_need(const FitArgs& a, int64_t id, int64_t* page) {
-    const int64_t u = id / a.pc.per_unit, slot = id - u * a.pc.per_unit;
-    const int64_t pg = a.pc.table[id];
-    const SlotWish w = slot_wish(a, u, slot, nullptr);
-    *page = pg;
-    if (!w.kept) return 0;
-    if (pg < 0) return 1;
-    const int32_t refs = a.refs[pg];
-    if (!w.written || refs <= 1) return 0;
-    return a.writers[pg] == static_cast<uint32_t>(refs) && a.last[pg] == id + 1 ? 0 : 2;
-}
-
-__global__ void __launch_bounds__(kThreads) fit_count_kernel(const FitArgs a, int slot_chunks) {
-    if (static_cast<int>(blockIdx.x) < slot_chunks) {
-        const int64_t slots = a.pc.n_units * a.pc.per_unit;
-        uint32_t need = 0, copy = 0;
-        for (int q = 0; q < kPageChunk / kThreads; ++q) {
-            const int64_t id = blockIdx.x * static_cast<int64_t>(kPageChunk) + q * kThreads + threadIdx.x;
-            int64_t pg;
-            const int w = id < slots ? slot_need(a, id, &pg) : 0;
-            need += w > 0;
-            copy += w == 2;
-        }
-        need = cta_sum(need);
-        copy = cta_sum(copy);
-        if (threadIdx.x == 0) a.slot_counts[blockIdx.x] = make_uint2(need, copy);
-    } else {
-        const int64_t c = blockIdx.x - slot_chunks;
-        uint32_t free = 0;
-        for (int q = 0; q < kPageChunk / kThreads; ++q) {
-            const int64_t p = c * kPageChunk + q * kThreads + threadIdx.x;
-            free += p < a.pc.n_pages && a.refs[p] == 0;
-        }
-        free = cta_sum(free);
-        if (threadIdx.x == 0) a.page_counts[c] = free;
+    if (!grid_barrier(a.barrier, 1, a.flag)) return;
+    // ---- requests, copies among them, free pages ----
+    uint32_t need = 0, copy = 0, free = 0;
+    for (int64_t id = s0 + tid; id < s1; id += kGridThreads) {
+        int64_t pg;
+        const int w = slot_need(a, id, &pg);
+        need += w > 0;
+        copy += w == 2;
     }
-}
-
-// The requests and the free pages in index order.  Nothing is served when
-// there are fewer free pages than requests.
-__global__ void __launch_bounds__(kThreads)
-fit_list_kernel(const FitArgs a, int slot_chunks, int page_chunks) {
-    const bool slots_side = static_cast<int>(blockIdx.x) < slot_chunks;
-    const int64_t c = slots_side ? blockIdx.x : blockIdx.x - slot_chunks;
-    const uint32_t* counts = reinterpret_cast<const uint32_t*>(a.slot_counts);
-    const uint2 need = cta_prefix(counts, 2, slot_chunks, slots_side ? c : 0);
-    const uint2 free = cta_prefix(a.page_counts, 1, page_chunks, slots_side ? 0 : c);
-    const bool served = need.y <= free.y;
-    if (blockIdx.x == 0) {
-        const uint2 copy = cta_prefix(counts + 1, 2, slot_chunks, 0);
-        if (threadIdx.x == 0) {
-            a.totals[0] = served ? need.y : 0;
-            a.totals[1] = served ? copy.y : 0;
-            if (!served) raise_flag(a.flag, TRI_FLAG_NO_PAGES);
-            if (a.n_free) *a.n_free = static_cast<int32_t>(free.y) - static_cast<int32_t>(need.y);
-        }
+    for (int64_t p = p0 + tid; p < p1; p += kGridThreads) free += __ldcg(a.refs + p) == 0;
+    need = cta_sum(need);
+    copy = cta_sum(copy);
+    free = cta_sum(free);
+    if (tid == 0) a.counts[c] = make_uint4(need, copy, free, 0);
+    if (!grid_barrier(a.barrier, 2, a.flag)) return;
+    // ---- both lists in index order; nothing is served when there are fewer
+    // free pages than requests ----
+    const PageSums sum = sum_counts(a.counts, static_cast<uint32_t>(c));
+    if (c == 0 && tid == 0) {
+        if (sum.all_x > sum.all_z) raise_flag(a.flag, TRI_FLAG_NO_PAGES);
+        if (a.n_free) *a.n_free = static_cast<int32_t>(sum.all_z) - static_cast<int32_t>(sum.all_x);
     }
-    if (!served || need.y == 0) return;
-    if (slots_side) {
-        if (a.slot_counts[c].x == 0) return;
-        const int64_t slots = a.pc.n_units * a.pc.per_unit;
-        uint32_t base = need.x, copy_base = cta_prefix(counts + 1, 2, slot_chunks, c).x;
-        for (int q = 0; q < kPageChunk / kThreads; ++q) {
-            const int64_t id = c * kPageChunk + q * kThreads + threadIdx.x;
+    if (sum.all_x == 0 || sum.all_x > sum.all_z) return;
+    if (need > 0) {
+        uint32_t base = sum.x, copy_base = sum.y;
+        for (int64_t b = s0; b < s1; b += kGridThreads) {
+            const int64_t id = b + tid;
             int64_t pg = -1;
-            const int w = id < slots ? slot_need(a, id, &pg) : 0;
+            const int w = id < s1 ? slot_need(a, id, &pg) : 0;
             uint32_t n, nc;
             const uint32_t r = base + cta_rank(w > 0, &n);
             const uint32_t rc = copy_base + cta_rank(w == 2, &nc);
@@ -352,76 +423,46 @@ fit_list_kernel(const FitArgs a, int slot_chunks, int page_chunks) {
             base += n;
             copy_base += nc;
         }
-    } else {
-        uint32_t base = free.x;
-        for (int q = 0; q < kPageChunk / kThreads && base < need.y; ++q) {
-            const int64_t p = c * kPageChunk + q * kThreads + threadIdx.x;
-            const bool is_free = p < a.pc.n_pages && a.refs[p] == 0;
-            uint32_t n;
-            const uint32_t r = base + cta_rank(is_free, &n);
-            if (is_free && r < need.y) a.free_page[r] = static_cast<int32_t>(p);
-            base += n;
-        }
     }
-}
-
-// A CTA copies `rows` rows of kVec 16-byte vectors, 8 loads a thread in
-// flight.
-__device__ __forceinline__ void copy_vectors(uint4* dst, const uint4* src, int64_t n) {
-    for (int64_t b = 0; b < n; b += 8 * kThreads) {
-        uint4 x[8];
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-            const int64_t e = b + q * kThreads + threadIdx.x;
-            if (e < n) x[q] = ld_stream(src + e);
-        }
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-            const int64_t e = b + q * kThreads + threadIdx.x;
-            if (e < n) dst[e] = x[q];
-        }
+    uint32_t base = sum.z;
+    for (int64_t b = p0; b < p1 && base < sum.all_x; b += kGridThreads) {
+        const int64_t p = b + tid;
+        const bool is_free = p < p1 && __ldcg(a.refs + p) == 0;
+        uint32_t n;
+        const uint32_t r = base + cta_rank(is_free, &n);
+        if (is_free && r < sum.all_x) a.free_page[r] = static_cast<int32_t>(p);
+        base += n;
     }
-}
-
-// Table entries and counts of the served requests, then the copies: a CTA
-// takes the K or the V rows of one page at a time.
-template <int kVec>
-__global__ void __launch_bounds__(kThreads) fit_serve_kernel(const FitArgs a) {
-    const uint32_t need = a.totals[0], copies = a.totals[1];
-    for (int64_t r = blockIdx.x * static_cast<int64_t>(kThreads) + threadIdx.x; r < need;
-         r += static_cast<int64_t>(gridDim.x) * kThreads) {
-        const int32_t pg = a.free_page[r], old = a.need_old[r];
-        a.pc.table[a.need_slot[r]] = pg;
+    if (!grid_barrier(a.barrier, 3, a.flag)) return;
+    // ---- table entries and counts of the requests, and the copies: a CTA
+    // takes 32 KB of the K or the V rows of a page at a time ----
+    for (int64_t r = c * kGridThreads + tid; r < sum.all_x; r += static_cast<int64_t>(gridDim.x) * kGridThreads) {
+        const int32_t pg = __ldcg(a.free_page + r), old = __ldcg(a.need_old + r);
+        a.pc.table[__ldcg(a.need_slot + r)] = pg;
         a.refs[pg] = 1;
         if (old >= 0) atomicSub(a.refs + old, 1);
     }
-    for (int64_t c = blockIdx.x; c < 2 * static_cast<int64_t>(copies); c += gridDim.x) {
-        const int32_t r = a.copy_rank[c >> 1];
-        const int64_t id = a.need_slot[r], old = a.need_old[r], pg = a.free_page[r];
-        const int64_t u = id / a.pc.per_unit;
-        const SlotWish w = slot_wish(a, u, id - u * a.pc.per_unit, nullptr);
-        uint4* x = static_cast<uint4*>(c & 1 ? a.v : a.k);
-        if (!x) continue;
-        copy_vectors(x + pg * a.pc.rows * kVec, x + old * a.pc.rows * kVec, w.rows * kVec);
+    const int64_t pieces = (a.pc.rows * kVec + kPiece - 1) / kPiece;
+    const int64_t items = 2 * pieces * sum.all_y;
+    for (int64_t it = c; it < items; it += gridDim.x) {
+        const int64_t page = it / (2 * pieces), x = it - page * 2 * pieces;
+        const int32_t r = __ldcg(a.copy_rank + page);
+        const int64_t id = __ldcg(a.need_slot + r), old = __ldcg(a.need_old + r), pg = __ldcg(a.free_page + r);
+        const uint32_t u = static_cast<uint32_t>(id) / per;
+        const SlotWish w = slot_wish(a, u, id - static_cast<int64_t>(u) * per, nullptr);
+        uint4* pool = static_cast<uint4*>(x & 1 ? a.v : a.k);
+        const int64_t at = (x >> 1) * kPiece, n = w.rows * kVec - at;
+        if (pool && n > 0)
+            copy_vectors(pool + pg * a.pc.rows * kVec + at, pool + old * a.pc.rows * kVec + at,
+                         n < kPiece ? n : kPiece);
     }
 }
 
+int page_ctas(int n_sm) { return 2 * n_sm; }
+
 cudaError_t launch_pages_fit(tri_dtype dt, const FitArgs& a, int n_sm, cudaStream_t s) {
-    const int64_t slots = a.pc.n_units * a.pc.per_unit;
-    const int slot_chunks = static_cast<int>((slots + kPageChunk - 1) / kPageChunk);
-    const int page_chunks = static_cast<int>((a.pc.n_pages + kPageChunk - 1) / kPageChunk);
-    fit_mark_kernel<<<grid_for(slots, kThreads, 8LL * n_sm), kThreads, 0, s>>>(a);
-    note_launch(s);
-    fit_count_kernel<<<slot_chunks + page_chunks, kThreads, 0, s>>>(a, slot_chunks);
-    note_launch(s);
-    fit_list_kernel<<<slot_chunks + page_chunks, kThreads, 0, s>>>(a, slot_chunks, page_chunks);
-    note_launch(s);
-    if (dt == TRI_BF16)
-        fit_serve_kernel<kD * 2 / 16><<<8 * n_sm, kThreads, 0, s>>>(a);
-    else
-        fit_serve_kernel<kD * 4 / 16><<<8 * n_sm, kThreads, 0, s>>>(a);
-    note_launch(s);
-    return cudaGetLastError();
+    return dt == TRI_BF16 ? launch_grid(pages_fit_kernel<kD * 2 / 16>, a, page_ctas(n_sm), s)
+                          : launch_grid(pages_fit_kernel<kD * 4 / 16>, a, page_ctas(n_sm), s);
 }
 
 // ---------------------------------------------------------------------------
@@ -431,9 +472,11 @@ cudaError_t launch_pages_fit(tri_dtype dt, const FitArgs& a, int n_sm, cudaStrea
 // read by some forks and replaced by another (beams that change places).  The
 // columns of the tables are independent of one another: a CTA takes some
 // columns of one (layer, head) for ALL forks, reads the sources' entries into
-// shared memory and only then writes the destinations'.  The row counts, which
-// every CTA reads, are replaced by the CTA that finishes last.
+// shared memory and only then writes the destinations'.  A warp takes a fork at
+// a time, its lanes neighbouring columns, kForkLoads of them in flight.  The
+// row counts, which every CTA reads, are replaced by the CTA that finishes last.
 constexpr int kForkCells = 8192;  // entries that a CTA holds
+constexpr int kForkLoads = 8;
 
 __global__ void __launch_bounds__(kThreads) pages_fork_kernel(const ForkArgs a, int table_cols,
                                                               int table_jobs, int pos_cols,
@@ -442,8 +485,9 @@ __global__ void __launch_bounds__(kThreads) pages_fork_kernel(const ForkArgs a, 
     int32_t* cell = reinterpret_cast<int32_t*>(smem);
     int32_t* src = cell + kForkCells;  // -1: empties, -2: skipped
     int32_t* dst = src + kMaxForks;
+    int32_t* rows = dst + kMaxForks;   // rows of the source unit
     __shared__ bool last;
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int F = static_cast<int>(a.n_fork);
     const int64_t per_seq = a.pc.n_units / a.pc.n_seq;  // (layer, head) pairs
     for (int f = tid; f < F; f += kThreads) {
@@ -472,55 +516,72 @@ __global__ void __launch_bounds__(kThreads) pages_fork_kernel(const ForkArgs a, 
             if (blockIdx.x == 0) raise_flag(a.flag, TRI_FLAG_INDEX_RANGE);
         }
     }
-    __syncthreads();
     const int64_t cap = a.pc.per_unit * a.pc.rows;
     const int64_t jobs = per_seq * (table_jobs + pos_jobs);
     for (int64_t job = blockIdx.x; job < jobs; job += gridDim.x) {
         const bool pos = job >= per_seq * table_jobs;
         const int64_t j = pos ? job - per_seq * table_jobs : job;
         const int64_t lh = j % per_seq;
-        const int64_t col0 = j / per_seq * (pos ? pos_cols : table_cols);
+        const int col0 = static_cast<int>(j / per_seq) * (pos ? pos_cols : table_cols);
         const int64_t width = pos ? a.cap : a.pc.per_unit;
         const int cols = static_cast<int>(min(static_cast<int64_t>(pos ? pos_cols : table_cols), width - col0));
-        for (int e = tid; e < F * cols; e += kThreads) {
-            const int f = e / cols, c = e - f * cols;
-            if (src[f] == -2) continue;
-            if (src[f] < 0) {
-                cell[e] = -1;
-                continue;
+        __syncthreads();
+        for (int f = tid; f < F; f += kThreads)
+            rows[f] = src[f] < 0 ? 0 : clamp_nvalid(a.n_valid, src[f] * per_seq + lh, cap, nullptr);
+        __syncthreads();
+        // Columns of the source that hold something: positions of rows, or
+        // pages of rows.
+        auto held = [&](int f) -> int {
+            const int n = pos ? rows[f]
+                              : static_cast<int>((static_cast<uint32_t>(rows[f]) + static_cast<uint32_t>(a.pc.rows) - 1u) /
+                                                 static_cast<uint32_t>(a.pc.rows));
+            return min(max(n - col0, 0), cols);
+        };
+        const int32_t* from = pos ? a.pos : a.pc.table;
+        for (int f = warp; f < F; f += kWarps) {
+            if (src[f] < 0) continue;
+            const int32_t* row = from + (src[f] * per_seq + lh) * width + col0;
+            const int n = held(f);
+            for (int c0 = lane; c0 < n; c0 += 32 * kForkLoads) {
+                int32_t x[kForkLoads];
+#pragma unroll
+                for (int q = 0; q < kForkLoads; ++q)
+                    if (c0 + 32 * q < n) x[q] = row[c0 + 32 * q];
+#pragma unroll
+                for (int q = 0; q < kForkLoads; ++q)
+                    if (c0 + 32 * q < n) cell[f * cols + c0 + 32 * q] = x[q];
             }
-            const int64_t u = src[f] * per_seq + lh;
-            const int64_t n = clamp_nvalid(a.n_valid, u, cap, nullptr);
-            if (pos) {
-                cell[e] = col0 + c < n ? a.pos[u * a.cap + col0 + c] : -1;
-                continue;
-            }
-            int32_t pg = -1;
-            if ((col0 + c) * a.pc.rows < n) {
-                pg = static_cast<int32_t>(page_of(a.pc, u, col0 + c));
-                if (pg < 0) raise_flag(a.flag, TRI_FLAG_INDEX_RANGE);
-            }
-            cell[e] = pg;
         }
         __syncthreads();
-        for (int e = tid; e < F * cols; e += kThreads) {
-            const int f = e / cols, c = e - f * cols;
+        for (int f = warp; f < F; f += kWarps) {
             if (src[f] == -2) continue;
-            const int64_t u = dst[f] * per_seq + lh;
+            const int n = held(f);
+            int32_t* row = (pos ? a.pos : a.pc.table) + (dst[f] * per_seq + lh) * width + col0;
             if (pos) {
-                if (src[f] < 0) continue;
-                const int64_t n = clamp_nvalid(a.n_valid, src[f] * per_seq + lh, cap, nullptr);
-                if (col0 + c < n) a.pos[u * a.cap + col0 + c] = cell[e];
+                for (int c = lane; c < n; c += 32) row[c] = cell[f * cols + c];
                 continue;
             }
-            const int64_t old = page_of(a.pc, u, col0 + c);
-            if (cell[e] != old) {
-                if (cell[e] >= 0) atomicAdd(a.refs + cell[e], 1);
-                if (old >= 0) atomicSub(a.refs + old, 1);
+            for (int c0 = lane; c0 < cols; c0 += 32 * kForkLoads) {
+                int32_t old[kForkLoads];
+#pragma unroll
+                for (int q = 0; q < kForkLoads; ++q)
+                    if (c0 + 32 * q < cols) old[q] = row[c0 + 32 * q];
+#pragma unroll
+                for (int q = 0; q < kForkLoads; ++q) {
+                    const int c = c0 + 32 * q;
+                    if (c >= cols) continue;
+                    int32_t now = c < n ? cell[f * cols + c] : -1;
+                    if (now < 0 || now >= a.pc.n_pages) {
+                        if (c < n) raise_flag(a.flag, TRI_FLAG_INDEX_RANGE);
+                        now = -1;
+                    }
+                    if (now == old[q]) continue;
+                    if (now >= 0) atomicAdd(a.refs + now, 1);
+                    if (old[q] >= 0 && old[q] < a.pc.n_pages) atomicSub(a.refs + old[q], 1);
+                    row[c] = now;
+                }
             }
-            a.pc.table[u * a.pc.per_unit + col0 + c] = cell[e];
         }
-        __syncthreads();
     }
     // ---- the counts, when every CTA has read them ----
     __threadfence();
@@ -531,15 +592,13 @@ __global__ void __launch_bounds__(kThreads) pages_fork_kernel(const ForkArgs a, 
     const int step = kForkCells / F;  // (layer, head) pairs at a time
     for (int64_t lh0 = 0; lh0 < per_seq; lh0 += step) {
         const int cols = static_cast<int>(min(static_cast<int64_t>(step), per_seq - lh0));
-        for (int e = tid; e < F * cols; e += kThreads) {
-            const int f = e / cols, c = e - f * cols;
-            cell[e] = src[f] >= 0 ? a.n_valid[src[f] * per_seq + lh0 + c] : 0;
-        }
+        for (int f = warp; f < F; f += kWarps)
+            for (int c = lane; c < cols; c += 32)
+                cell[f * cols + c] = src[f] >= 0 ? __ldcg(a.n_valid + src[f] * per_seq + lh0 + c) : 0;
         __syncthreads();
-        for (int e = tid; e < F * cols; e += kThreads) {
-            const int f = e / cols, c = e - f * cols;
-            if (src[f] != -2) a.n_valid[dst[f] * per_seq + lh0 + c] = cell[e];
-        }
+        for (int f = warp; f < F; f += kWarps)
+            for (int c = lane; c < cols; c += 32)
+                if (src[f] != -2) a.n_valid[dst[f] * per_seq + lh0 + c] = cell[f * cols + c];
         __syncthreads();
     }
     if (!a.p_cur) return;
@@ -557,15 +616,23 @@ __global__ void __launch_bounds__(kThreads) pages_fork_kernel(const ForkArgs a, 
     }
 }
 
-cudaError_t launch_pages_fork(const ForkArgs& a, cudaStream_t s) {
-    const int64_t most = kForkCells / a.n_fork;
-    const int table_cols = static_cast<int>(a.pc.per_unit < most ? a.pc.per_unit : most);
-    const int64_t pos_width = a.pos ? a.cap : 0;
-    const int pos_cols = static_cast<int>(pos_width < most ? (pos_width ? pos_width : 1) : most);
+cudaError_t launch_pages_fork(const ForkArgs& a, int n_sm, cudaStream_t s) {
     const int64_t per_seq = a.pc.n_units / a.pc.n_seq;
+    // Columns of a job: what fits the cells, but not so many that the jobs
+    // leave the SMs (4 CTAs each) without work; 32 at least.
+    const int64_t most = kForkCells / a.n_fork;
+    auto columns = [&](int64_t width) {
+        int64_t c = (width * per_seq + 4 * n_sm - 1) / (4 * n_sm);
+        c = c < 32 ? 32 : c;
+        c = c < most ? c : most;
+        return static_cast<int>(c < width ? c : width);
+    };
+    const int64_t pos_width = a.pos ? a.cap : 0;
+    const int table_cols = columns(a.pc.per_unit), pos_cols = pos_width ? columns(pos_width) : 1;
     const int table_jobs = static_cast<int>((a.pc.per_unit + table_cols - 1) / table_cols);
     const int pos_jobs = static_cast<int>((pos_width + pos_cols - 1) / pos_cols);
-    constexpr size_t smem = (kForkCells + 2 * kMaxForks) * sizeof(int32_t);
+    constexpr size_t smem = (kForkCells + 3 * kMaxForks) * sizeof(int32_t);
+    static_assert(smem <= 48 * 1024, "more than the default limit");
     pages_fork_kernel<<<grid_for(per_seq * (table_jobs + pos_jobs), 1, 65535), kThreads, smem, s>>>(
         a, table_cols, table_jobs, pos_cols, pos_jobs);
     note_launch(s);
@@ -577,37 +644,34 @@ cudaError_t launch_pages_fork(const ForkArgs& a, cudaStream_t s) {
 // ---------------------------------------------------------------------------
 // With L live pages, the live pages at L and behind go, in order, to the free
 // pages below L, in order (there are as many of one as of the other).
-__global__ void __launch_bounds__(kThreads) compact_count_kernel(const CompactPagesArgs a) {
-    uint32_t live = 0;
-    for (int q = 0; q < kPageChunk / kThreads; ++q) {
-        const int64_t p = blockIdx.x * static_cast<int64_t>(kPageChunk) + q * kThreads + threadIdx.x;
-        live += p < a.pc.n_pages && a.refs[p] != 0;
-    }
-    live = cta_sum(live);
-    if (threadIdx.x == 0) a.page_counts[blockIdx.x] = live;
-}
-
-__global__ void __launch_bounds__(kThreads) compact_list_kernel(const CompactPagesArgs a, int chunks) {
+template <int kVec>
+__global__ void __launch_bounds__(kGridThreads, 2) pages_compact_kernel(const CompactPagesArgs a) {
+    const int tid = threadIdx.x;
     const int64_t c = blockIdx.x;
-    const uint2 live = cta_prefix(a.page_counts, 1, chunks, c);
-    const int64_t L = live.y;
-    // Live pages below L: whole chunks, then the chunk that L lies in.
-    const int64_t cl = L / kPageChunk;
-    uint32_t below = cta_prefix(a.page_counts, 1, chunks, cl).x, part = 0;
-    for (int64_t p = cl * kPageChunk + threadIdx.x; p < L; p += kThreads) part += a.refs[p] != 0;
-    below += cta_sum(part);
-    if (c == 0 && threadIdx.x == 0) {
-        a.totals[0] = static_cast<uint32_t>(L);
-        a.totals[1] = static_cast<uint32_t>(L) - below;
-        if (a.n_live) *a.n_live = static_cast<int32_t>(L);
-    }
-    uint32_t base = live.x;
-    for (int q = 0; q < kPageChunk / kThreads; ++q) {
-        const int64_t p = c * kPageChunk + q * kThreads + threadIdx.x;
-        const bool is_live = p < a.pc.n_pages && a.refs[p] != 0;
+    const int64_t p0 = part_begin(a.pc.n_pages, c), p1 = part_begin(a.pc.n_pages, c + 1);
+    uint32_t live = 0;
+    for (int64_t p = p0 + tid; p < p1; p += kGridThreads) live += a.refs[p] != 0;
+    live = cta_sum(live);
+    if (tid == 0) a.counts[c] = make_uint4(live, 0, 0, 0);
+    if (!grid_barrier(a.barrier, 1, a.flag)) return;
+    const int64_t L = sum_counts(a.counts, 0).all_x;
+    // Live pages below L: those of whole parts, then of the part that L lies in.
+    int64_t cl = L * gridDim.x / a.pc.n_pages;
+    while (cl + 1 < gridDim.x && part_begin(a.pc.n_pages, cl + 1) <= L) ++cl;
+    while (cl > 0 && part_begin(a.pc.n_pages, cl) > L) --cl;
+    uint32_t some = 0;
+    for (int64_t p = part_begin(a.pc.n_pages, cl) + tid; p < L; p += kGridThreads) some += a.refs[p] != 0;
+    const uint32_t below = sum_counts(a.counts, static_cast<uint32_t>(cl)).x + cta_sum(some);
+    const int64_t moves = L - below;
+    if (c == 0 && tid == 0 && a.n_live) *a.n_live = static_cast<int32_t>(L);
+    if (moves == 0) return;
+    uint32_t base = sum_counts(a.counts, static_cast<uint32_t>(c)).x;
+    for (int64_t b = p0; b < p1; b += kGridThreads) {
+        const int64_t p = b + tid;
+        const bool is_live = p < p1 && a.refs[p] != 0;
         uint32_t n;
         const uint32_t r = base + cta_rank(is_live, &n);  // live pages before p
-        if (p < a.pc.n_pages) {
+        if (p < p1) {
             if (p < L && !is_live) a.to[p - r] = static_cast<int32_t>(p);
             if (p >= L && is_live) {
                 a.from[r - below] = static_cast<int32_t>(p);
@@ -616,50 +680,37 @@ __global__ void __launch_bounds__(kThreads) compact_list_kernel(const CompactPag
         }
         base += n;
     }
-}
-
-// The moving pages' rows and counts, and the table entries that name them.
-template <int kVec>
-__global__ void __launch_bounds__(kThreads) compact_move_kernel(const CompactPagesArgs a) {
-    const int64_t L = a.totals[0], moves = a.totals[1];
-    if (moves == 0) return;
+    if (!grid_barrier(a.barrier, 2, a.flag)) return;
+    // ---- the table entries that name the moving pages, their counts and rows ----
     const int64_t slots = a.pc.n_units * a.pc.per_unit;
-    for (int64_t id = blockIdx.x * static_cast<int64_t>(kThreads) + threadIdx.x; id < slots;
-         id += static_cast<int64_t>(gridDim.x) * kThreads) {
+    for (int64_t id = c * kGridThreads + tid; id < slots; id += static_cast<int64_t>(gridDim.x) * kGridThreads) {
         const int64_t pg = a.pc.table[id];
         if (pg < L || pg >= a.pc.n_pages) continue;
         // An entry whose page's count is 0 names no listed page: left, flagged.
-        const int64_t r = a.rank[pg];
-        if (r >= 0 && r < moves && a.from[r] == pg)
-            a.pc.table[id] = a.to[r];
+        const int64_t r = __ldcg(a.rank + pg);
+        if (r >= 0 && r < moves && __ldcg(a.from + r) == pg)
+            a.pc.table[id] = __ldcg(a.to + r);
         else
             raise_flag(a.flag, TRI_FLAG_INDEX_RANGE);
     }
-    for (int64_t c = blockIdx.x; c < 2 * moves; c += gridDim.x) {
-        const int64_t from = a.from[c >> 1], to = a.to[c >> 1];
-        if ((c & 1) == 0 && threadIdx.x == 0) {
+    const int64_t vecs = a.pc.rows * kVec, pieces = (vecs + kPiece - 1) / kPiece;
+    for (int64_t it = c; it < 2 * pieces * moves; it += gridDim.x) {
+        const int64_t m = it / (2 * pieces), x = it - m * 2 * pieces;
+        const int64_t from = __ldcg(a.from + m), to = __ldcg(a.to + m);
+        if (x == 0 && tid == 0) {
             a.refs[to] = a.refs[from];
             a.refs[from] = 0;
         }
-        uint4* x = static_cast<uint4*>(c & 1 ? a.v : a.k);
-        if (!x) continue;
-        copy_vectors(x + to * a.pc.rows * kVec, x + from * a.pc.rows * kVec, a.pc.rows * kVec);
+        uint4* pool = static_cast<uint4*>(x & 1 ? a.v : a.k);
+        const int64_t at = (x >> 1) * kPiece, n = vecs - at;
+        if (pool) copy_vectors(pool + to * vecs + at, pool + from * vecs + at, n < kPiece ? n : kPiece);
     }
 }
 
 cudaError_t launch_pages_compact(tri_dtype dt, const CompactPagesArgs& a, int n_sm,
                                  cudaStream_t s) {
-    const int chunks = static_cast<int>((a.pc.n_pages + kPageChunk - 1) / kPageChunk);
-    compact_count_kernel<<<chunks, kThreads, 0, s>>>(a);
-    note_launch(s);
-    compact_list_kernel<<<chunks, kThreads, 0, s>>>(a, chunks);
-    note_launch(s);
-    if (dt == TRI_BF16)
-        compact_move_kernel<kD * 2 / 16><<<8 * n_sm, kThreads, 0, s>>>(a);
-    else
-        compact_move_kernel<kD * 4 / 16><<<8 * n_sm, kThreads, 0, s>>>(a);
-    note_launch(s);
-    return cudaGetLastError();
+    return dt == TRI_BF16 ? launch_grid(pages_compact_kernel<kD * 2 / 16>, a, page_ctas(n_sm), s)
+                          : launch_grid(pages_compact_kernel<kD * 4 / 16>, a, page_ctas(n_sm), s);
 }
 
 }  // namespace tri
