@@ -532,8 +532,9 @@ tri_status tri_append(void* k_cache, void* v_cache, int32_t* pos_cache, tri_dtyp
  * pools [n_pages][page_rows][head_dim] (dt) and a device page table
  * [n_units][pages_per_unit] int32, entry -1 where a unit has no page; row j of
  * unit u is row j % page_rows of page page_table[u][j / page_rows].  page_rows
- * is any number >= 1 here (the prune wants a multiple of 128), n_pages *
- * page_rows and n_units * pages_per_unit at most 2^31 - 1.  An entry below
+ * is any number from 1 to 2^26 here (the prune wants a multiple of 128), n_pages *
+ * page_rows, n_units * pages_per_unit and pages_per_unit * page_rows at most
+ * 2^31 - 1.  An entry below
  * -1 or >= n_pages sets TRI_FLAG_INDEX_RANGE where it is met and counts as no
  * page.  page_refs (device, [n_pages] int32) counts the table entries that
  * name a page; 0: the page is free.  The caller starts with a table of -1 and

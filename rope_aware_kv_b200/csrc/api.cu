@@ -520,7 +520,7 @@ tri_status check_paged(tri_dtype dt, int head_dim, int64_t n_seq, int64_t n_unit
         page_rows < 1 || pages_per_unit < 1 || n_pages < 1)
         return TRI_ERR_INVALID_ARG;
     if (!dtype_ok(dt) || head_dim != kD) return TRI_ERR_UNSUPPORTED;
-    if (n_seq > INT32_MAX || n_units > INT32_MAX || page_rows > INT32_MAX / n_pages ||
+    if (n_seq > INT32_MAX || n_units > INT32_MAX || page_rows > (1 << 26) || page_rows > INT32_MAX / n_pages ||
         pages_per_unit > INT32_MAX / n_units || pages_per_unit > INT32_MAX / page_rows)
         return TRI_ERR_UNSUPPORTED;
     return TRI_OK;
@@ -567,18 +567,21 @@ DecodePagedWs decode_paged_ws(int64_t n_units, int G) {
 }
 
 struct PagesWs {
-    size_t writers, last, zero_end, counts, list[4], total;
+    size_t done, done_end, writers, last, zero_end, counts, list[3], copies, total;
 };
 PagesWs pages_ws(int64_t n_units, int64_t pages_per_unit, int64_t n_pages) {
     PagesWs w;
     const int64_t slots = n_units * pages_per_unit;
     Carve c;
+    w.done = c.take(static_cast<size_t>(n_units) * 4);
+    w.done_end = c.off;
     w.writers = c.take(static_cast<size_t>(n_pages) * 4);
     w.last = c.take(static_cast<size_t>(n_pages) * 4);
     w.zero_end = c.off;
     w.counts = c.take(static_cast<size_t>(page_ctas(static_cast<int>(sm_count_or_default()))) * 16);
     const size_t most = static_cast<size_t>(slots < n_pages ? slots : n_pages);
     for (size_t& l : w.list) l = c.take(most * 4);
+    w.copies = c.take(most * 16);
     w.total = c.off;
     return w;
 }
@@ -1360,8 +1363,8 @@ tri_status tri_pages_fit(void* k_pool, void* v_pool, tri_dtype dt, int64_t n_seq
     a.counts = reinterpret_cast<uint4*>(ws_at(ws, w.counts));
     a.need_slot = reinterpret_cast<int32_t*>(ws_at(ws, w.list[0]));
     a.need_old = reinterpret_cast<int32_t*>(ws_at(ws, w.list[1]));
-    a.copy_rank = reinterpret_cast<int32_t*>(ws_at(ws, w.list[2]));
-    a.free_page = reinterpret_cast<int32_t*>(ws_at(ws, w.list[3]));
+    a.free_page = reinterpret_cast<int32_t*>(ws_at(ws, w.list[2]));
+    a.copies = reinterpret_cast<int4*>(ws_at(ws, w.copies));
     a.barrier = ws_flag(ws) + 1;
     a.flag = ws_flag(ws);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -1383,9 +1386,10 @@ tri_status tri_pages_fork(int32_t* page_table, int64_t page_rows, int64_t pages_
     if (!aligned4(page_refs) || !aligned4(n_valid) || !aligned4(src_seq) || !aligned4(dst_seq) ||
         !aligned4(pos) || (reinterpret_cast<uintptr_t>(p_cur) & 7))
         return TRI_ERR_INVALID_ARG;
-    TRI_TRY(check_pages_ws(ws, ws_bytes, pages_ws(n_units, pages_per_unit, n_pages)));
+    const PagesWs w = pages_ws(n_units, pages_per_unit, n_pages);
+    TRI_TRY(check_pages_ws(ws, ws_bytes, w));
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    TRI_CUDA(cudaMemsetAsync(ws, 0, kWsHeader, s));
+    TRI_CUDA(cudaMemsetAsync(ws, 0, w.done_end, s));
     if (n_fork == 0) return TRI_OK;
     ForkArgs a;
     a.pc = paged_cache(page_table, page_rows, pages_per_unit, n_pages, n_seq, n_units);
@@ -1397,7 +1401,7 @@ tri_status tri_pages_fork(int32_t* page_table, int64_t page_rows, int64_t pages_
     a.src = src_seq;
     a.dst = dst_seq;
     a.n_fork = n_fork;
-    a.done = ws_flag(ws) + 1;
+    a.done = reinterpret_cast<uint32_t*>(ws_at(ws, w.done));
     a.flag = ws_flag(ws);
     return cuda_status(launch_pages_fork(a, static_cast<int>(sm_count_or_default()), s));
 }

@@ -104,7 +104,7 @@ struct FitArgs {
     uint4* counts;            // [ctas]: pages asked for, of them copies, free pages
     int32_t* need_slot;       // [min(slots, pages)]: the i-th request's slot
     int32_t* need_old;        //   and the page it copies (-1: none)
-    int32_t* copy_rank;       // [min(slots, pages)]: the requests that copy
+    int4* copies;             // [min(slots, pages)]: page that is copied, request, rows
     int32_t* free_page;       // [min(slots, pages)]: the i-th free page
     uint32_t* barrier;        // zero on entry
     uint32_t* flag;
@@ -123,7 +123,7 @@ struct ForkArgs {
     const int32_t* src;
     const int32_t* dst;
     int64_t n_fork;
-    uint32_t* done;           // zero on entry: CTAs that are done
+    uint32_t* done;           // [n_units / n_seq], zero on entry: jobs that are done
     uint32_t* flag;
 };
 cudaError_t launch_pages_fork(const ForkArgs& a, int n_sm, cudaStream_t s);

@@ -142,17 +142,43 @@ __global__ void __launch_bounds__(kThreads) append_few_kernel(const AppendPagedA
     append_account(a, i, r, lane);
 }
 
-// Many: the units are looked over first (one warp each), then every CTA
-// copies kAppendChunk rows of one unit.
+// Many: the units are looked over first (a CTA each, since a unit's positions
+// and pages are many), then every CTA copies kAppendChunk rows of one unit.
 constexpr int kAppendChunk = 64;
 
 __global__ void __launch_bounds__(kThreads) append_look_kernel(const AppendPagedArgs a) {
-    const int lane = threadIdx.x & 31;
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-    if (i >= a.sl.n) return;
-    const AppendUnit r = append_check(a, i, lane);
-    if (lane == 0) a.first[i] = static_cast<int32_t>(r.first);
-    append_account(a, i, r, lane);
+    const int tid = threadIdx.x;
+    const int64_t i = blockIdx.x;
+    const int64_t u = slice_unit(a.sl, i);
+    const int64_t seq = u / (a.pc.n_units / a.pc.n_seq);
+    const int64_t add = rows_added(a.n_add, seq, a.n_new, tid == 0 ? a.flag : nullptr);
+    const int64_t n = a.n_valid[u];
+    uint32_t bad = n < 0 || n + add > a.cap ? TRI_FLAG_NVALID_RANGE : 0;
+    int32_t best = INT32_MIN;
+    if (!bad && add > 0) {
+        const int64_t s1 = (n + add - 1) / a.pc.rows;
+        for (int64_t slot = n / a.pc.rows + tid; slot <= s1; slot += kThreads) {
+            const int64_t pg = page_of(a.pc, u, slot);
+            if (pg < 0)
+                bad |= TRI_FLAG_INDEX_RANGE;
+            else if (a.refs && a.refs[pg] > 1)
+                bad |= TRI_FLAG_SHARED_PAGE;
+        }
+        if (a.p_cur) {
+#pragma unroll 8
+            for (int64_t x = tid; x < add; x += kThreads) best = max(best, a.pos_new[i * a.n_new + x]);
+        }
+    }
+    const int any = __syncthreads_or(bad != 0);
+    if (bad) raise_flag(a.flag, bad);
+    if (tid == 0) {
+        a.first[i] = any ? -1 : static_cast<int32_t>(n);
+        if (!any) a.n_valid[u] = static_cast<int32_t>(n + add);
+    }
+    if (any || add == 0 || !a.p_cur) return;
+    best = __reduce_max_sync(0xffffffffu, best);
+    if ((tid & 31) == 0 && best != INT32_MIN)
+        atomicMax(reinterpret_cast<long long*>(a.p_cur) + seq, static_cast<long long>(best) + 1);
 }
 
 template <int kVec>
@@ -171,13 +197,12 @@ __global__ void __launch_bounds__(kThreads) append_copy_kernel(const AppendPaged
 
 template <int kVec>
 static cudaError_t launch_append_t(const AppendPagedArgs& a, cudaStream_t s) {
-    const unsigned units = grid_for(a.sl.n, kWarps, INT32_MAX);
     if (a.n_new <= kAppendFew) {
-        append_few_kernel<kVec><<<units, kThreads, 0, s>>>(a);
+        append_few_kernel<kVec><<<grid_for(a.sl.n, kWarps, INT32_MAX), kThreads, 0, s>>>(a);
         note_launch(s);
         return cudaGetLastError();
     }
-    append_look_kernel<<<units, kThreads, 0, s>>>(a);
+    append_look_kernel<<<static_cast<unsigned>(a.sl.n), kThreads, 0, s>>>(a);
     note_launch(s);
     const int64_t chunks = (a.n_new + kAppendChunk - 1) / kAppendChunk;
     append_copy_kernel<kVec><<<static_cast<unsigned>(a.sl.n * chunks), kThreads, 0, s>>>(
@@ -197,7 +222,7 @@ cudaError_t launch_append_paged(tri_dtype dt, const AppendPagedArgs& a, cudaStre
 // depend on one another over the whole pool, and a barrier of the grid costs
 // less than a launch.  CTA c of C owns the c-th C-th of the slots and of the
 // pages, so ranks over the pool are prefix sums of C counts.
-constexpr int kGridThreads = 512;
+constexpr int kGridThreads = 1024;
 constexpr int kGridWarps = kGridThreads / 32;
 
 // All CTAs of the grid have arrived (their writes are visible); `round` counts
@@ -260,55 +285,113 @@ __device__ __forceinline__ uint32_t cta_rank(bool x, uint32_t* total) {
     return before;
 }
 
-// Sums of the CTAs' counts x, y, z before CTA `at` and of all CTAs.
+// Sums of the CTAs' counts x, y, z before CTA `at` and of all CTAs, by one
+// warp for the CTA.
 struct PageSums {
     uint32_t x, y, z, all_x, all_y, all_z;
 };
 __device__ __forceinline__ PageSums sum_counts(const uint4* counts, uint32_t at) {
-    PageSums s = {};
-    for (uint32_t c = threadIdx.x; c < gridDim.x; c += kGridThreads) {
-        const uint4 v = __ldcg(counts + c);
-        s.all_x += v.x;
-        s.all_y += v.y;
-        s.all_z += v.z;
-        if (c < at) {
-            s.x += v.x;
-            s.y += v.y;
-            s.z += v.z;
+    __shared__ PageSums out;
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        PageSums s = {};
+        for (uint32_t c = threadIdx.x; c < gridDim.x; c += 32) {
+            const uint4 v = __ldcg(counts + c);
+            s.all_x += v.x;
+            s.all_y += v.y;
+            s.all_z += v.z;
+            if (c < at) {
+                s.x += v.x;
+                s.y += v.y;
+                s.z += v.z;
+            }
         }
+        s.x = __reduce_add_sync(0xffffffffu, s.x);
+        s.y = __reduce_add_sync(0xffffffffu, s.y);
+        s.z = __reduce_add_sync(0xffffffffu, s.z);
+        s.all_x = __reduce_add_sync(0xffffffffu, s.all_x);
+        s.all_y = __reduce_add_sync(0xffffffffu, s.all_y);
+        s.all_z = __reduce_add_sync(0xffffffffu, s.all_z);
+        if (threadIdx.x == 0) out = s;
     }
-    s.x = cta_sum(s.x);
-    s.y = cta_sum(s.y);
-    s.z = cta_sum(s.z);
-    s.all_x = cta_sum(s.all_x);
-    s.all_y = cta_sum(s.all_y);
-    s.all_z = cta_sum(s.all_z);
-    return s;
+    __syncthreads();
+    return out;
 }
 
-// n 16-byte vectors, kLoads a thread in flight.
-constexpr int kLoads = 4;
-constexpr int kPiece = kLoads * kGridThreads;  // vectors that a CTA copies at a time: 32 KB
+// Copies of whole or part pages, of K and then of V, as one flat run of bytes
+// (`page_bytes` a page) cut into windows.  Every warp moves a window at a time
+// through its own 6 KB of shared memory with bulk copies, lane x the part of
+// the window that lies in its x-th page, so pages of any size keep 192 KB an SM
+// in flight.  page(c) gives copy c's source and destination page and its bytes.
+// (Loads and stores through registers, 64 KB an SM in flight, moved 698 MB in
+// 161 us; three kernels of them with 256 KB in 130 us.)
+constexpr int kWindow = 6144;  // 24 pages of one bf16 row
+struct CopyShared {
+    unsigned char window[kGridWarps][kWindow];
+    uint64_t landed[kGridWarps];
+};
 
-__device__ __forceinline__ void copy_vectors(uint4* dst, const uint4* src, int64_t n) {
-    uint4 x[kLoads];
-#pragma unroll
-    for (int q = 0; q < kLoads; ++q) {
-        const int64_t e = q * kGridThreads + threadIdx.x;
-        if (e < n) x[q] = ld_stream(src + e);
+struct PageCopy {
+    int32_t from, to;
+    int64_t bytes;
+};
+
+template <typename Page>
+__device__ __forceinline__ void copy_pages(void* k, void* v, int64_t copies, int64_t page_bytes,
+                                           uint32_t* flag, Page page) {
+    extern __shared__ __align__(16) unsigned char smem[];
+    CopyShared& sm = *reinterpret_cast<CopyShared*>(smem);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    unsigned char* window = sm.window[warp];
+    uint64_t* landed = &sm.landed[warp];
+    if (lane == 0) {
+        mbar_init(landed, 1);
+        fence_barrier_init();
     }
-#pragma unroll
-    for (int q = 0; q < kLoads; ++q) {
-        const int64_t e = q * kGridThreads + threadIdx.x;
-        if (e < n) dst[e] = x[q];
+    __syncwarp();
+    uint32_t phase = 0;
+    const int64_t all = copies * page_bytes;
+    const int64_t windows = (all + kWindow - 1) / kWindow;
+    for (int64_t w = static_cast<int64_t>(warp) * gridDim.x + blockIdx.x; w < windows * (v ? 2 : 1);
+         w += static_cast<int64_t>(gridDim.x) * kGridWarps) {
+        const bool second = w >= windows;
+        char* pool = static_cast<char*>(second ? v : k);
+        const int64_t b0 = (second ? w - windows : w) * kWindow, b1 = min(b0 + kWindow, all);
+        const int64_t c = b0 / page_bytes + lane;
+        const int64_t at = max(b0, c * page_bytes);
+        // This lane's part: bytes [at, at + n) of the run, off within page c.
+        int64_t off = 0, n = 0;
+        PageCopy p = {0, 0, 0};
+        if (at < b1) {
+            p = page(c);
+            off = at - c * page_bytes;
+            n = max(min(min(b1 - at, page_bytes - off), p.bytes - off), static_cast<int64_t>(0));
+        }
+        const uint32_t bytes = __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(n));
+        bulk_wait_read<0>();  // this lane's last part has left the window
+        __syncwarp();
+        if (bytes == 0) continue;
+        if (lane == 0) mbar_arrive_expect_tx(landed, bytes);
+        __syncwarp();
+        if (n > 0)
+            bulk_load(window + (at - b0), pool + p.from * page_bytes + off, static_cast<uint32_t>(n), landed);
+        const bool ok = mbar_wait(landed, phase, flag);
+        phase ^= 1;
+        if (!__all_sync(0xffffffffu, ok)) break;
+        if (n > 0) bulk_store(pool + p.to * page_bytes + off, window + (at - b0), static_cast<uint32_t>(n));
+        bulk_commit();
     }
+    bulk_wait_all();
 }
 
 template <typename Args>
 static cudaError_t launch_grid(void (*fn)(Args), const Args& a, int ctas, cudaStream_t s) {
     void* args[1] = {const_cast<Args*>(&a)};
-    const cudaError_t e = cudaLaunchCooperativeKernel(reinterpret_cast<const void*>(fn), dim3(ctas),
-                                                      dim3(kGridThreads), args, 0, s);
+    const void* f = reinterpret_cast<const void*>(fn);
+    constexpr size_t smem = sizeof(CopyShared);
+    cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    e = cudaLaunchCooperativeKernel(f, dim3(ctas), dim3(kGridThreads), args, smem, s);
     if (e == cudaSuccess) note_launch(s);
     return e;
 }
@@ -355,8 +438,8 @@ __device__ __forceinline__ int slot_need(const FitArgs& a, int64_t id, int64_t* 
     return __ldcg(a.writers + pg) == static_cast<uint32_t>(refs) && __ldcg(a.last + pg) == id + 1 ? 0 : 2;
 }
 
-template <int kVec>
-__global__ void __launch_bounds__(kGridThreads, 2) pages_fit_kernel(const FitArgs a) {
+template <int kRow>  // bytes of a row
+__global__ void __launch_bounds__(kGridThreads, 1) pages_fit_kernel(const FitArgs a) {
     const int tid = threadIdx.x;
     const int64_t c = blockIdx.x;
     const int64_t slots = a.pc.n_units * a.pc.per_unit;
@@ -419,7 +502,12 @@ __global__ void __launch_bounds__(kGridThreads, 2) pages_fit_kernel(const FitArg
                 a.need_slot[r] = static_cast<int32_t>(id);
                 a.need_old[r] = w == 2 ? static_cast<int32_t>(pg) : -1;
             }
-            if (w == 2) a.copy_rank[rc] = static_cast<int32_t>(r);
+            if (w == 2) {
+                const uint32_t u = static_cast<uint32_t>(id) / per;
+                const int64_t rows = slot_wish(a, u, id - static_cast<int64_t>(u) * per, nullptr).rows;
+                a.copies[rc] = make_int4(static_cast<int32_t>(pg), static_cast<int32_t>(r),
+                                         static_cast<int32_t>(rows), 0);
+            }
             base += n;
             copy_base += nc;
         }
@@ -434,35 +522,24 @@ __global__ void __launch_bounds__(kGridThreads, 2) pages_fit_kernel(const FitArg
         base += n;
     }
     if (!grid_barrier(a.barrier, 3, a.flag)) return;
-    // ---- table entries and counts of the requests, and the copies: a CTA
-    // takes 32 KB of the K or the V rows of a page at a time ----
+    // ---- table entries and counts of the requests, and the copies ----
     for (int64_t r = c * kGridThreads + tid; r < sum.all_x; r += static_cast<int64_t>(gridDim.x) * kGridThreads) {
         const int32_t pg = __ldcg(a.free_page + r), old = __ldcg(a.need_old + r);
         a.pc.table[__ldcg(a.need_slot + r)] = pg;
         a.refs[pg] = 1;
         if (old >= 0) atomicSub(a.refs + old, 1);
     }
-    const int64_t pieces = (a.pc.rows * kVec + kPiece - 1) / kPiece;
-    const int64_t items = 2 * pieces * sum.all_y;
-    for (int64_t it = c; it < items; it += gridDim.x) {
-        const int64_t page = it / (2 * pieces), x = it - page * 2 * pieces;
-        const int32_t r = __ldcg(a.copy_rank + page);
-        const int64_t id = __ldcg(a.need_slot + r), old = __ldcg(a.need_old + r), pg = __ldcg(a.free_page + r);
-        const uint32_t u = static_cast<uint32_t>(id) / per;
-        const SlotWish w = slot_wish(a, u, id - static_cast<int64_t>(u) * per, nullptr);
-        uint4* pool = static_cast<uint4*>(x & 1 ? a.v : a.k);
-        const int64_t at = (x >> 1) * kPiece, n = w.rows * kVec - at;
-        if (pool && n > 0)
-            copy_vectors(pool + pg * a.pc.rows * kVec + at, pool + old * a.pc.rows * kVec + at,
-                         n < kPiece ? n : kPiece);
-    }
+    copy_pages(a.k, a.v, sum.all_y, a.pc.rows * kRow, a.flag, [&](int64_t x) {
+        const int4 y = __ldcg(a.copies + x);
+        return PageCopy{y.x, __ldcg(a.free_page + y.y), static_cast<int64_t>(y.z) * kRow};
+    });
 }
 
-int page_ctas(int n_sm) { return 2 * n_sm; }
+int page_ctas(int n_sm) { return n_sm; }
 
 cudaError_t launch_pages_fit(tri_dtype dt, const FitArgs& a, int n_sm, cudaStream_t s) {
-    return dt == TRI_BF16 ? launch_grid(pages_fit_kernel<kD * 2 / 16>, a, page_ctas(n_sm), s)
-                          : launch_grid(pages_fit_kernel<kD * 4 / 16>, a, page_ctas(n_sm), s);
+    return dt == TRI_BF16 ? launch_grid(pages_fit_kernel<kD * 2>, a, page_ctas(n_sm), s)
+                          : launch_grid(pages_fit_kernel<kD * 4>, a, page_ctas(n_sm), s);
 }
 
 // ---------------------------------------------------------------------------
@@ -474,7 +551,8 @@ cudaError_t launch_pages_fit(tri_dtype dt, const FitArgs& a, int n_sm, cudaStrea
 // columns of one (layer, head) for ALL forks, reads the sources' entries into
 // shared memory and only then writes the destinations'.  A warp takes a fork at
 // a time, its lanes neighbouring columns, kForkLoads of them in flight.  The
-// row counts, which every CTA reads, are replaced by the CTA that finishes last.
+// row counts of a (layer, head), which all its jobs read, are replaced by the
+// CTA that finishes the last of them.
 constexpr int kForkCells = 8192;  // entries that a CTA holds
 constexpr int kForkLoads = 8;
 
@@ -516,6 +594,21 @@ __global__ void __launch_bounds__(kThreads) pages_fork_kernel(const ForkArgs a, 
             if (blockIdx.x == 0) raise_flag(a.flag, TRI_FLAG_INDEX_RANGE);
         }
     }
+    __syncthreads();
+    if (a.p_cur && blockIdx.x == 0) {
+        int64_t now[kMaxForks / kThreads];
+#pragma unroll
+        for (int q = 0; q < kMaxForks / kThreads; ++q) {
+            const int f = q * kThreads + tid;
+            now[q] = f < F && src[f] >= 0 ? a.p_cur[src[f]] : 0;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int q = 0; q < kMaxForks / kThreads; ++q) {
+            const int f = q * kThreads + tid;
+            if (f < F && src[f] != -2) a.p_cur[dst[f]] = now[q];
+        }
+    }
     const int64_t cap = a.pc.per_unit * a.pc.rows;
     const int64_t jobs = per_seq * (table_jobs + pos_jobs);
     for (int64_t job = blockIdx.x; job < jobs; job += gridDim.x) {
@@ -528,9 +621,8 @@ __global__ void __launch_bounds__(kThreads) pages_fork_kernel(const ForkArgs a, 
         __syncthreads();
         for (int f = tid; f < F; f += kThreads)
             rows[f] = src[f] < 0 ? 0 : clamp_nvalid(a.n_valid, src[f] * per_seq + lh, cap, nullptr);
-        __syncthreads();
-        // Columns of the source that hold something: positions of rows, or
-        // pages of rows.
+        // (The sources are read without waiting for their counts.)  Columns
+        // of the source that hold something: positions of rows, or pages.
         auto held = [&](int f) -> int {
             const int n = pos ? rows[f]
                               : static_cast<int>((static_cast<uint32_t>(rows[f]) + static_cast<uint32_t>(a.pc.rows) - 1u) /
@@ -541,15 +633,14 @@ __global__ void __launch_bounds__(kThreads) pages_fork_kernel(const ForkArgs a, 
         for (int f = warp; f < F; f += kWarps) {
             if (src[f] < 0) continue;
             const int32_t* row = from + (src[f] * per_seq + lh) * width + col0;
-            const int n = held(f);
-            for (int c0 = lane; c0 < n; c0 += 32 * kForkLoads) {
+            for (int c0 = lane; c0 < cols; c0 += 32 * kForkLoads) {
                 int32_t x[kForkLoads];
 #pragma unroll
                 for (int q = 0; q < kForkLoads; ++q)
-                    if (c0 + 32 * q < n) x[q] = row[c0 + 32 * q];
+                    if (c0 + 32 * q < cols) x[q] = row[c0 + 32 * q];
 #pragma unroll
                 for (int q = 0; q < kForkLoads; ++q)
-                    if (c0 + 32 * q < n) cell[f * cols + c0 + 32 * q] = x[q];
+                    if (c0 + 32 * q < cols) cell[f * cols + c0 + 32 * q] = x[q];
             }
         }
         __syncthreads();
@@ -582,37 +673,19 @@ __global__ void __launch_bounds__(kThreads) pages_fork_kernel(const ForkArgs a, 
                 }
             }
         }
-    }
-    // ---- the counts, when every CTA has read them ----
-    __threadfence();
-    __syncthreads();
-    if (tid == 0) last = atomicAdd(a.done, 1u) == gridDim.x - 1;
-    __syncthreads();
-    if (!last) return;
-    const int step = kForkCells / F;  // (layer, head) pairs at a time
-    for (int64_t lh0 = 0; lh0 < per_seq; lh0 += step) {
-        const int cols = static_cast<int>(min(static_cast<int64_t>(step), per_seq - lh0));
-        for (int f = warp; f < F; f += kWarps)
-            for (int c = lane; c < cols; c += 32)
-                cell[f * cols + c] = src[f] >= 0 ? __ldcg(a.n_valid + src[f] * per_seq + lh0 + c) : 0;
+        // ---- the counts, when every job of the (layer, head) has read them ----
         __syncthreads();
-        for (int f = warp; f < F; f += kWarps)
-            for (int c = lane; c < cols; c += 32)
-                if (src[f] != -2) a.n_valid[dst[f] * per_seq + lh0 + c] = cell[f * cols + c];
+        if (tid == 0) {
+            __threadfence();
+            last = atomicAdd(a.done + lh, 1u) == static_cast<uint32_t>(table_jobs + pos_jobs) - 1;
+        }
         __syncthreads();
-    }
-    if (!a.p_cur) return;
-    int64_t now[kMaxForks / kThreads];
-#pragma unroll
-    for (int q = 0; q < kMaxForks / kThreads; ++q) {
-        const int f = q * kThreads + tid;
-        now[q] = f < F && src[f] >= 0 ? a.p_cur[src[f]] : 0;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int q = 0; q < kMaxForks / kThreads; ++q) {
-        const int f = q * kThreads + tid;
-        if (f < F && src[f] != -2) a.p_cur[dst[f]] = now[q];
+        if (!last) continue;
+        for (int f = tid; f < F; f += kThreads)
+            cell[f] = src[f] >= 0 ? a.n_valid[src[f] * per_seq + lh] : 0;
+        __syncthreads();
+        for (int f = tid; f < F; f += kThreads)
+            if (src[f] != -2) a.n_valid[dst[f] * per_seq + lh] = cell[f];
     }
 }
 
@@ -644,8 +717,8 @@ cudaError_t launch_pages_fork(const ForkArgs& a, int n_sm, cudaStream_t s) {
 // ---------------------------------------------------------------------------
 // With L live pages, the live pages at L and behind go, in order, to the free
 // pages below L, in order (there are as many of one as of the other).
-template <int kVec>
-__global__ void __launch_bounds__(kGridThreads, 2) pages_compact_kernel(const CompactPagesArgs a) {
+template <int kRow>  // bytes of a row
+__global__ void __launch_bounds__(kGridThreads, 1) pages_compact_kernel(const CompactPagesArgs a) {
     const int tid = threadIdx.x;
     const int64_t c = blockIdx.x;
     const int64_t p0 = part_begin(a.pc.n_pages, c), p1 = part_begin(a.pc.n_pages, c + 1);
@@ -654,7 +727,8 @@ __global__ void __launch_bounds__(kGridThreads, 2) pages_compact_kernel(const Co
     live = cta_sum(live);
     if (tid == 0) a.counts[c] = make_uint4(live, 0, 0, 0);
     if (!grid_barrier(a.barrier, 1, a.flag)) return;
-    const int64_t L = sum_counts(a.counts, 0).all_x;
+    const PageSums sum = sum_counts(a.counts, static_cast<uint32_t>(c));
+    const int64_t L = sum.all_x;
     // Live pages below L: those of whole parts, then of the part that L lies in.
     int64_t cl = L * gridDim.x / a.pc.n_pages;
     while (cl + 1 < gridDim.x && part_begin(a.pc.n_pages, cl + 1) <= L) ++cl;
@@ -665,7 +739,7 @@ __global__ void __launch_bounds__(kGridThreads, 2) pages_compact_kernel(const Co
     const int64_t moves = L - below;
     if (c == 0 && tid == 0 && a.n_live) *a.n_live = static_cast<int32_t>(L);
     if (moves == 0) return;
-    uint32_t base = sum_counts(a.counts, static_cast<uint32_t>(c)).x;
+    uint32_t base = sum.x;
     for (int64_t b = p0; b < p1; b += kGridThreads) {
         const int64_t p = b + tid;
         const bool is_live = p < p1 && a.refs[p] != 0;
@@ -693,24 +767,21 @@ __global__ void __launch_bounds__(kGridThreads, 2) pages_compact_kernel(const Co
         else
             raise_flag(a.flag, TRI_FLAG_INDEX_RANGE);
     }
-    const int64_t vecs = a.pc.rows * kVec, pieces = (vecs + kPiece - 1) / kPiece;
-    for (int64_t it = c; it < 2 * pieces * moves; it += gridDim.x) {
-        const int64_t m = it / (2 * pieces), x = it - m * 2 * pieces;
-        const int64_t from = __ldcg(a.from + m), to = __ldcg(a.to + m);
-        if (x == 0 && tid == 0) {
-            a.refs[to] = a.refs[from];
-            a.refs[from] = 0;
-        }
-        uint4* pool = static_cast<uint4*>(x & 1 ? a.v : a.k);
-        const int64_t at = (x >> 1) * kPiece, n = vecs - at;
-        if (pool) copy_vectors(pool + to * vecs + at, pool + from * vecs + at, n < kPiece ? n : kPiece);
+    for (int64_t m = c * kGridThreads + tid; m < moves; m += static_cast<int64_t>(gridDim.x) * kGridThreads) {
+        const int32_t from = __ldcg(a.from + m), to = __ldcg(a.to + m);
+        a.refs[to] = a.refs[from];
+        a.refs[from] = 0;
     }
+    const int64_t page_bytes = a.pc.rows * kRow;
+    copy_pages(a.k, a.v, moves, page_bytes, a.flag, [&](int64_t x) {
+        return PageCopy{__ldcg(a.from + x), __ldcg(a.to + x), page_bytes};
+    });
 }
 
 cudaError_t launch_pages_compact(tri_dtype dt, const CompactPagesArgs& a, int n_sm,
                                  cudaStream_t s) {
-    return dt == TRI_BF16 ? launch_grid(pages_compact_kernel<kD * 2 / 16>, a, page_ctas(n_sm), s)
-                          : launch_grid(pages_compact_kernel<kD * 4 / 16>, a, page_ctas(n_sm), s);
+    return dt == TRI_BF16 ? launch_grid(pages_compact_kernel<kD * 2>, a, page_ctas(n_sm), s)
+                          : launch_grid(pages_compact_kernel<kD * 4>, a, page_ctas(n_sm), s);
 }
 
 }  // namespace tri
