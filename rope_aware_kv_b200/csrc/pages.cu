@@ -222,7 +222,7 @@ cudaError_t launch_append_paged(tri_dtype dt, const AppendPagedArgs& a, cudaStre
 // depend on one another over the whole pool, and a barrier of the grid costs
 // less than a launch.  CTA c of C owns the c-th C-th of the slots and of the
 // pages, so ranks over the pool are prefix sums of C counts.
-constexpr int kGridThreads = 1024;
+constexpr int kGridThreads = 512;
 constexpr int kGridWarps = kGridThreads / 32;
 
 // All CTAs of the grid have arrived (their writes are visible); `round` counts
@@ -320,12 +320,13 @@ __device__ __forceinline__ PageSums sum_counts(const uint4* counts, uint32_t at)
 
 // Copies of whole or part pages, of K and then of V, as one flat run of bytes
 // (`page_bytes` a page) cut into windows.  Every warp moves a window at a time
-// through its own 6 KB of shared memory with bulk copies, lane x the part of
+// through its own 12 KB of shared memory with bulk copies, lane x the part of
 // the window that lies in its x-th page, so pages of any size keep 192 KB an SM
 // in flight.  page(c) gives copy c's source and destination page and its bytes.
-// (Loads and stores through registers, 64 KB an SM in flight, moved 698 MB in
-// 161 us; three kernels of them with 256 KB in 130 us.)
-constexpr int kWindow = 6144;  // 24 pages of one bf16 row
+// A compaction that moves 698 MB takes 135 us (5.8 TB/s for the rows); 138 us
+// with 32 windows of 6 KB, 144 us with 64 of 3 KB, and 161 us with loads and
+// stores through registers (64 KB an SM in flight).
+constexpr int kWindow = 12288;
 struct CopyShared {
     unsigned char window[kGridWarps][kWindow];
     uint64_t landed[kGridWarps];
@@ -351,12 +352,13 @@ __device__ __forceinline__ void copy_pages(void* k, void* v, int64_t copies, int
     __syncwarp();
     uint32_t phase = 0;
     const int64_t all = copies * page_bytes;
-    const int64_t windows = (all + kWindow - 1) / kWindow;
+    const int64_t window_bytes = min(static_cast<int64_t>(kWindow), 31 * page_bytes);  // 32 pages at most
+    const int64_t windows = (all + window_bytes - 1) / window_bytes;
     for (int64_t w = static_cast<int64_t>(warp) * gridDim.x + blockIdx.x; w < windows * (v ? 2 : 1);
          w += static_cast<int64_t>(gridDim.x) * kGridWarps) {
         const bool second = w >= windows;
         char* pool = static_cast<char*>(second ? v : k);
-        const int64_t b0 = (second ? w - windows : w) * kWindow, b1 = min(b0 + kWindow, all);
+        const int64_t b0 = (second ? w - windows : w) * window_bytes, b1 = min(b0 + window_bytes, all);
         const int64_t c = b0 / page_bytes + lane;
         const int64_t at = max(b0, c * page_bytes);
         // This lane's part: bytes [at, at + n) of the run, off within page c.
@@ -384,12 +386,12 @@ __device__ __forceinline__ void copy_pages(void* k, void* v, int64_t copies, int
     bulk_wait_all();
 }
 
-template <typename Args>
+template <typename Key, typename Args>
 static cudaError_t launch_grid(void (*fn)(Args), const Args& a, int ctas, cudaStream_t s) {
     void* args[1] = {const_cast<Args*>(&a)};
     const void* f = reinterpret_cast<const void*>(fn);
     constexpr size_t smem = sizeof(CopyShared);
-    cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    cudaError_t e = allow_smem<Key>(f, smem);
     if (e != cudaSuccess) return e;
     e = cudaLaunchCooperativeKernel(f, dim3(ctas), dim3(kGridThreads), args, smem, s);
     if (e == cudaSuccess) note_launch(s);
@@ -538,8 +540,10 @@ __global__ void __launch_bounds__(kGridThreads, 1) pages_fit_kernel(const FitArg
 int page_ctas(int n_sm) { return n_sm; }
 
 cudaError_t launch_pages_fit(tri_dtype dt, const FitArgs& a, int n_sm, cudaStream_t s) {
-    return dt == TRI_BF16 ? launch_grid(pages_fit_kernel<kD * 2>, a, page_ctas(n_sm), s)
-                          : launch_grid(pages_fit_kernel<kD * 4>, a, page_ctas(n_sm), s);
+    struct Bf16 {};
+    struct F32 {};
+    return dt == TRI_BF16 ? launch_grid<Bf16>(pages_fit_kernel<kD * 2>, a, page_ctas(n_sm), s)
+                          : launch_grid<F32>(pages_fit_kernel<kD * 4>, a, page_ctas(n_sm), s);
 }
 
 // ---------------------------------------------------------------------------
@@ -549,15 +553,14 @@ cudaError_t launch_pages_fit(tri_dtype dt, const FitArgs& a, int n_sm, cudaStrea
 // read by some forks and replaced by another (beams that change places).  The
 // columns of the tables are independent of one another: a CTA takes some
 // columns of one (layer, head) for ALL forks, reads the sources' entries into
-// shared memory and only then writes the destinations'.  A warp takes a fork at
-// a time, its lanes neighbouring columns, kForkLoads of them in flight.  The
+// shared memory and only then writes the destinations'.  The
 // row counts of a (layer, head), which all its jobs read, are replaced by the
 // CTA that finishes the last of them.
 constexpr int kForkCells = 8192;  // entries that a CTA holds
-constexpr int kForkLoads = 8;
+constexpr int kForkLoads = 4;
 
-__global__ void __launch_bounds__(kThreads) pages_fork_kernel(const ForkArgs a, int table_cols,
-                                                              int table_jobs, int pos_cols,
+__global__ void __launch_bounds__(kThreads) pages_fork_kernel(const ForkArgs a, int table_bits,
+                                                              int table_jobs, int pos_bits,
                                                               int pos_jobs) {
     extern __shared__ __align__(16) unsigned char smem[];
     int32_t* cell = reinterpret_cast<int32_t*>(smem);
@@ -615,61 +618,56 @@ __global__ void __launch_bounds__(kThreads) pages_fork_kernel(const ForkArgs a, 
         const bool pos = job >= per_seq * table_jobs;
         const int64_t j = pos ? job - per_seq * table_jobs : job;
         const int64_t lh = j % per_seq;
-        const int col0 = static_cast<int>(j / per_seq) * (pos ? pos_cols : table_cols);
+        const int bits = pos ? pos_bits : table_bits;  // 2^bits columns
+        const int col0 = static_cast<int>(j / per_seq) << bits;
         const int64_t width = pos ? a.cap : a.pc.per_unit;
-        const int cols = static_cast<int>(min(static_cast<int64_t>(pos ? pos_cols : table_cols), width - col0));
+        const int cols = static_cast<int>(min(int64_t(1) << bits, width - col0));
         __syncthreads();
         for (int f = tid; f < F; f += kThreads)
             rows[f] = src[f] < 0 ? 0 : clamp_nvalid(a.n_valid, src[f] * per_seq + lh, cap, nullptr);
-        // (The sources are read without waiting for their counts.)  Columns
-        // of the source that hold something: positions of rows, or pages.
-        auto held = [&](int f) -> int {
-            const int n = pos ? rows[f]
-                              : static_cast<int>((static_cast<uint32_t>(rows[f]) + static_cast<uint32_t>(a.pc.rows) - 1u) /
-                                                 static_cast<uint32_t>(a.pc.rows));
-            return min(max(n - col0, 0), cols);
-        };
-        const int32_t* from = pos ? a.pos : a.pc.table;
+        // A warp takes a fork at a time, its lanes neighbouring columns.  The
+        // sources go straight to shared memory, all of them in flight, and
+        // without waiting for their counts.
+        int32_t* table = pos ? a.pos : a.pc.table;
         for (int f = warp; f < F; f += kWarps) {
-            if (src[f] < 0) continue;
-            const int32_t* row = from + (src[f] * per_seq + lh) * width + col0;
-            for (int c0 = lane; c0 < cols; c0 += 32 * kForkLoads) {
-                int32_t x[kForkLoads];
-#pragma unroll
-                for (int q = 0; q < kForkLoads; ++q)
-                    if (c0 + 32 * q < cols) x[q] = row[c0 + 32 * q];
-#pragma unroll
-                for (int q = 0; q < kForkLoads; ++q)
-                    if (c0 + 32 * q < cols) cell[f * cols + c0 + 32 * q] = x[q];
-            }
+            if (src[f] < 0 || (pos && src[f] == dst[f])) continue;
+            const int32_t* from = table + (src[f] * per_seq + lh) * width + col0;
+            int32_t* to = cell + (f << bits);
+            for (int c = lane; c < cols; c += 32)
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(to + c)), "l"(from + c)
+                             : "memory");
         }
+        asm volatile("cp.async.wait_all;" ::: "memory");
         __syncthreads();
         for (int f = warp; f < F; f += kWarps) {
-            if (src[f] == -2) continue;
-            const int n = held(f);
-            int32_t* row = (pos ? a.pos : a.pc.table) + (dst[f] * per_seq + lh) * width + col0;
+            if (src[f] == -2 || (pos && src[f] == dst[f])) continue;
+            int32_t* to = table + (dst[f] * per_seq + lh) * width + col0;
+            const int32_t* from = cell + (f << bits);
             if (pos) {
-                for (int c = lane; c < n; c += 32) row[c] = cell[f * cols + c];
+                const int n = min(rows[f] - col0, cols);
+                for (int c = lane; c < n; c += 32) to[c] = from[c];
                 continue;
             }
             for (int c0 = lane; c0 < cols; c0 += 32 * kForkLoads) {
                 int32_t old[kForkLoads];
 #pragma unroll
                 for (int q = 0; q < kForkLoads; ++q)
-                    if (c0 + 32 * q < cols) old[q] = row[c0 + 32 * q];
+                    if (c0 + 32 * q < cols) old[q] = to[c0 + 32 * q];
 #pragma unroll
                 for (int q = 0; q < kForkLoads; ++q) {
                     const int c = c0 + 32 * q;
                     if (c >= cols) continue;
-                    int32_t now = c < n ? cell[f * cols + c] : -1;
+                    // A page that holds rows of the source, or none.
+                    const bool held = static_cast<int64_t>(col0 + c) * a.pc.rows < rows[f];
+                    int32_t now = held ? from[c] : -1;
                     if (now < 0 || now >= a.pc.n_pages) {
-                        if (c < n) raise_flag(a.flag, TRI_FLAG_INDEX_RANGE);
+                        if (held) raise_flag(a.flag, TRI_FLAG_INDEX_RANGE);
                         now = -1;
                     }
                     if (now == old[q]) continue;
                     if (now >= 0) atomicAdd(a.refs + now, 1);
                     if (old[q] >= 0 && old[q] < a.pc.n_pages) atomicSub(a.refs + old[q], 1);
-                    row[c] = now;
+                    to[c] = now;
                 }
             }
         }
@@ -691,23 +689,22 @@ __global__ void __launch_bounds__(kThreads) pages_fork_kernel(const ForkArgs a, 
 
 cudaError_t launch_pages_fork(const ForkArgs& a, int n_sm, cudaStream_t s) {
     const int64_t per_seq = a.pc.n_units / a.pc.n_seq;
-    // Columns of a job: what fits the cells, but not so many that the jobs
-    // leave the SMs (4 CTAs each) without work; 32 at least.
-    const int64_t most = kForkCells / a.n_fork;
-    auto columns = [&](int64_t width) {
-        int64_t c = (width * per_seq + 4 * n_sm - 1) / (4 * n_sm);
-        c = c < 32 ? 32 : c;
-        c = c < most ? c : most;
-        return static_cast<int>(c < width ? c : width);
+    // Columns of a job, a power of two: what fits the cells, but not so many
+    // that the jobs leave the SMs (4 CTAs each) without work; 32 at least.
+    auto bits = [&](int64_t width) {
+        int b = 5;
+        while ((int64_t(1) << b) < width && (width >> b) * per_seq > 4 * n_sm) ++b;
+        while (b > 0 && (a.n_fork << b) > kForkCells) --b;
+        return b;
     };
     const int64_t pos_width = a.pos ? a.cap : 0;
-    const int table_cols = columns(a.pc.per_unit), pos_cols = pos_width ? columns(pos_width) : 1;
-    const int table_jobs = static_cast<int>((a.pc.per_unit + table_cols - 1) / table_cols);
-    const int pos_jobs = static_cast<int>((pos_width + pos_cols - 1) / pos_cols);
+    const int table_bits = bits(a.pc.per_unit), pos_bits = bits(pos_width);
+    const int table_jobs = static_cast<int>((a.pc.per_unit + (int64_t(1) << table_bits) - 1) >> table_bits);
+    const int pos_jobs = static_cast<int>((pos_width + (int64_t(1) << pos_bits) - 1) >> pos_bits);
     constexpr size_t smem = (kForkCells + 3 * kMaxForks) * sizeof(int32_t);
     static_assert(smem <= 48 * 1024, "more than the default limit");
     pages_fork_kernel<<<grid_for(per_seq * (table_jobs + pos_jobs), 1, 65535), kThreads, smem, s>>>(
-        a, table_cols, table_jobs, pos_cols, pos_jobs);
+        a, table_bits, table_jobs, pos_bits, pos_jobs);
     note_launch(s);
     return cudaGetLastError();
 }
@@ -780,8 +777,10 @@ __global__ void __launch_bounds__(kGridThreads, 1) pages_compact_kernel(const Co
 
 cudaError_t launch_pages_compact(tri_dtype dt, const CompactPagesArgs& a, int n_sm,
                                  cudaStream_t s) {
-    return dt == TRI_BF16 ? launch_grid(pages_compact_kernel<kD * 2>, a, page_ctas(n_sm), s)
-                          : launch_grid(pages_compact_kernel<kD * 4>, a, page_ctas(n_sm), s);
+    struct Bf16 {};
+    struct F32 {};
+    return dt == TRI_BF16 ? launch_grid<Bf16>(pages_compact_kernel<kD * 2>, a, page_ctas(n_sm), s)
+                          : launch_grid<F32>(pages_compact_kernel<kD * 4>, a, page_ctas(n_sm), s);
 }
 
 }  // namespace tri
