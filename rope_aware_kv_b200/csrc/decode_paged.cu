@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) decode_paged_rows_kernel(const
     const int sub = lane & 7, quad = lane >> 3;  // lane of a key, key of four
     const int64_t cap = a.pc.per_unit * a.pc.rows;
     const SplitPlan p = plan_split<kRowThreads>(a, kRowTile, kRowWarps);
-    SplitUnit split[2] = {};
+    SplitUnit split0 = {}, split1 = {};
     int n_split = 0;
     unsigned char* ring = sm.ring[warp];
     float* pw = sm.p[warp];
@@ -229,15 +229,14 @@ __global__ void __launch_bounds__(kRowThreads, 1) decode_paged_rows_kernel(const
             // ---- online softmax of my_head ----
             const uint32_t bits = have >> (gi * kGroup + quad);
             const bool va = bits & 1, vb = bits & 16;
-            const float xa = va ? sa[0] * a.scale_log2 : -INFINITY;
-            const float xb = vb ? sb[0] * a.scale_log2 : -INFINITY;
-            float mx = fmaxf(xa, xb);
+            float mx = fmaxf(va ? sa[0] * a.scale_log2 : -INFINITY, vb ? sb[0] * a.scale_log2 : -INFINITY);
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
             const float m_new = fmaxf(m, mx);
             const float base = m_new == -INFINITY ? 0.f : m_new;
-            const float wa = va ? exp2f(xa - base) : 0.f;
-            const float wb = vb ? exp2f(xb - base) : 0.f;
+            // (one rounding of the small difference, not of the large product)
+            const float wa = va ? exp2f(fmaf(sa[0], a.scale_log2, -base)) : 0.f;
+            const float wb = vb ? exp2f(fmaf(sb[0], a.scale_log2, -base)) : 0.f;
             if (__any_sync(0xffffffffu, m_new != m)) {
                 const float al = exp2f(m - base);
                 l *= al;
@@ -327,16 +326,15 @@ __global__ void __launch_bounds__(kRowThreads, 1) decode_paged_rows_kernel(const
             }
         }
         if (!whole) {
-            split[0] = n_split ? split[0] : SplitUnit{i, tile0, n_tiles, false};
-            split[1] = SplitUnit{i, tile0, n_tiles, false};
-            ++n_split;
+            split1 = split_unit(p, i, tile0, n_tiles);
+            if (n_split++ == 0) split0 = split1;
         }
         __syncthreads();  // red and Q are rewritten by the next unit
         t = tile0 + b1;
         tile0 += n_tiles;
         ++i;
     }
-    join_split_units<kRowWarps, 0, 8>(a, G, p, n_split, split);
+    join_split_units<kRowWarps, 0, 8>(a, G, n_split, split0, split1);
     write_empty_units(a, G);
 }
 

@@ -138,7 +138,7 @@ decode_paged_tc_kernel(const __grid_constant__ CUtensorMap kmap,
         smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023));
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t cap = a.pc.per_unit * a.pc.rows;
-    if (tid == 0) {
+    if (tid == kTcMath) {
         for (int i = 0; i < kTcStages; ++i) {
             mbar_init(&sm.k_full[i], 1);
             mbar_init(&sm.k_empty[i], 1);
@@ -153,15 +153,19 @@ decode_paged_tc_kernel(const __grid_constant__ CUtensorMap kmap,
         prefetch_tensormap(&kmap);
         prefetch_tensormap(&vmap);
     }
-    if (warp == 0) tc_alloc(&sm.tmem, 64);
-    // Columns 24 .. 31 of the weights stay zeros.
-    if (tid < kTcMath)
+    const SplitPlan p = plan_split<kTcThreads>(a, kTcTile, 1);  // (synchronises the CTA)
+    // The loading warp goes on while the others get their tensor memory.
+    uint32_t tmem = 0;
+    if (warp < kTcMath / 32) {
+        if (warp == 0) tc_alloc(&sm.tmem, 64);
+        // Columns 24 .. 31 of the weights stay zeros.
         *reinterpret_cast<uint4*>(sm.p + tid * kTcPRow + ((3 ^ ((tid >> 1) & 3)) * 16)) =
             make_uint4(0, 0, 0, 0);
-    tc_fence_before();
-    const SplitPlan p = plan_split<kTcThreads>(a, kTcTile, 1);  // (synchronises the CTA)
-    tc_fence_after();
-    const uint32_t tmem = sm.tmem;
+        tc_fence_before();
+        named_sync(1, kTcMath);
+        tc_fence_after();
+        tmem = sm.tmem;
+    }
 
     uint32_t it = 0;  // tiles of this CTA so far
     uint32_t t = p.begin, i = p.unit, tile0 = p.tile0;
@@ -171,7 +175,7 @@ decode_paged_tc_kernel(const __grid_constant__ CUtensorMap kmap,
         const uint64_t pol = policy_evict_first();
         for (; t < p.end; ++i) {
             const int64_t u = slice_unit(a.sl, i);
-            const uint32_t n = clamp_nvalid(a.n_valid, u, cap, nullptr);
+            const uint32_t n = i == p.unit ? p.rows : clamp_nvalid(a.n_valid, u, cap, nullptr);
             const uint32_t n_tiles = static_cast<uint32_t>(n + kTcTile - 1) / kTcTile;
             if (n_tiles == 0) continue;
             const uint32_t t1 = min(tile0 + n_tiles, p.end);
@@ -219,12 +223,12 @@ decode_paged_tc_kernel(const __grid_constant__ CUtensorMap kmap,
         const uint32_t lanes = static_cast<uint32_t>(warp) * 32 << 16;  // this warp's TMEM lanes
         const uint32_t s_cols = tmem, o_cols = tmem + 32;
         const uint32_t page_rows = static_cast<uint32_t>(a.pc.rows);
-        SplitUnit split[2] = {};
+        SplitUnit split0 = {}, split1 = {};
         int n_split = 0;
         bool ok = true;
         while (t < p.end) {
             const int64_t u = slice_unit(a.sl, i);
-            const uint32_t n = clamp_nvalid(a.n_valid, u, cap, nullptr);
+            const uint32_t n = i == p.unit ? p.rows : clamp_nvalid(a.n_valid, u, cap, nullptr);
             const uint32_t n_tiles = static_cast<uint32_t>(n + kTcTile - 1) / kTcTile;
             if (n_tiles == 0) {
                 ++i;
@@ -278,8 +282,7 @@ decode_paged_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                 float x[8];
 #pragma unroll
                 for (int h = 0; h < 8; ++h) {
-                    if (h < G) s[h] = valid ? s[h] * a.scale_log2 : -INFINITY;
-                    x[h] = h < G ? s[h] : -INFINITY;
+                    x[h] = h < G && valid ? s[h] * a.scale_log2 : -INFINITY;
                 }
 #pragma unroll
                 for (int q = 0; q < 3; ++q) {
@@ -308,7 +311,8 @@ decode_paged_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                     const float m_new = fmaxf(m[h], mt);
                     const float base = m_new == -INFINITY ? 0.f : m_new;
                     al[h] = exp2f(m[h] - base);
-                    const float w = valid ? exp2f(s[h] - base) : 0.f;
+                    // (one rounding of the small difference, not of the large product)
+                    const float w = valid ? exp2f(fmaf(s[h], a.scale_log2, -base)) : 0.f;
                     l[h] = fmaf(l[h], al[h], w);
                     m[h] = m_new;
                     s[h] = w;
@@ -387,16 +391,15 @@ decode_paged_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                 }
             }
             if (!whole) {
-                split[0] = n_split ? split[0] : SplitUnit{i, tile0, n_tiles, false};
-                split[1] = SplitUnit{i, tile0, n_tiles, false};
-                ++n_split;
+                split1 = split_unit(p, i, tile0, n_tiles);
+                if (n_split++ == 0) split0 = split1;
             }
             named_sync(1, kTcMath);  // wsum and Q are rewritten by the next unit
             tile0 += n_tiles;
             ++i;
         }
         if (!*reinterpret_cast<volatile int*>(&sm.abort))
-            join_split_units<kTcMath / 32, 1, 16>(a, G, p, n_split, split);
+            join_split_units<kTcMath / 32, 1, 16>(a, G, n_split, split0, split1);
     }
     wait_for_clear();
     write_empty_units(a, G);

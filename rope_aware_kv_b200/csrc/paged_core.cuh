@@ -44,6 +44,7 @@ struct SplitPlan {
     uint32_t end;
     uint32_t unit;    // first unit of the range
     uint32_t tile0;   // its first tile
+    uint32_t rows;    // its rows
 };
 
 __device__ __forceinline__ uint32_t range_begin(const SplitPlan& p, uint32_t c) {
@@ -63,18 +64,22 @@ __device__ __forceinline__ uint32_t cta_of_tile(const SplitPlan& p, uint32_t t) 
 template <int kThreads>
 __device__ SplitPlan plan_split(const DecodePagedArgs& a, int tile, uint32_t min_tiles) {
     __shared__ uint32_t warp_sum[kThreads / 32];
-    __shared__ uint32_t found[2];
+    __shared__ uint32_t found[3];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t cap = a.pc.per_unit * a.pc.rows;
     const uint32_t units = static_cast<uint32_t>(a.sl.n);
     const uint32_t per = (units + kThreads - 1) / kThreads;
     const uint32_t i0 = min(tid * per, units), i1 = min(i0 + per, units);
-    auto tiles = [&](uint32_t i) -> uint32_t {
-        return static_cast<uint32_t>(clamp_nvalid(a.n_valid, slice_unit(a.sl, i), cap, nullptr) + (tile - 1)) / tile;
+    auto rows_of = [&](uint32_t i) -> uint32_t {
+        return clamp_nvalid(a.n_valid, slice_unit(a.sl, i), cap, nullptr);
     };
-    uint32_t sum = 0;
+    uint32_t sum = 0, n0 = 0;
 #pragma unroll 4
-    for (uint32_t i = i0; i < i1; ++i) sum += tiles(i);
+    for (uint32_t i = i0; i < i1; ++i) {
+        const uint32_t n = rows_of(i);
+        if (i == i0) n0 = n;
+        sum += (n + (tile - 1)) / tile;
+    }
     uint32_t incl = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -99,10 +104,11 @@ __device__ SplitPlan plan_split(const DecodePagedArgs& a, int tile, uint32_t min
     if (p.begin < p.end && before <= p.begin && p.begin < before + sum) {
         uint32_t t = before;
         for (uint32_t i = i0; i < i1; ++i) {
-            const uint32_t nt = per == 1 ? sum : tiles(i);
+            const uint32_t n = i == i0 ? n0 : rows_of(i), nt = (n + (tile - 1)) / tile;
             if (p.begin < t + nt) {
                 found[0] = i;
                 found[1] = t;
+                found[2] = n;
                 break;
             }
             t += nt;
@@ -111,6 +117,7 @@ __device__ SplitPlan plan_split(const DecodePagedArgs& a, int tile, uint32_t min
     __syncthreads();
     p.unit = found[0];
     p.tile0 = found[1];
+    p.rows = found[2];
     return p;
 }
 
@@ -179,156 +186,169 @@ __device__ __forceinline__ uint32_t part_slot(const SplitPlan& p, uint32_t c, ui
 }
 
 // A CTA's range holds at most two units that lie in other ranges too: its
-// first and its last.
+// first and its last.  The partials of such a unit: n of them, of CTAs c0,
+// c0 + 1, ..., the first in slot0, the others in slots 2 c.
 struct SplitUnit {
-    uint32_t i, tile0, n_tiles;
-    bool last;  // this CTA joins it
+    uint32_t i, c0, n, slot0;
 };
+__device__ __forceinline__ SplitUnit split_unit(const SplitPlan& p, uint32_t i, uint32_t tile0,
+                                                uint32_t n_tiles) {
+    SplitUnit s;
+    s.i = i;
+    s.c0 = cta_of_tile(p, tile0);
+    s.n = cta_of_tile(p, tile0 + n_tiles - 1) - s.c0 + 1;
+    s.slot0 = part_slot(p, s.c0, tile0);
+    return s;
+}
+// Row of head h of the unit's x-th partial; x past the last one repeats it.
+__device__ __forceinline__ uint32_t part_row(const SplitUnit& s, uint32_t x, int G, int h) {
+    x = min(x, s.n - 1);
+    return (x == 0 ? s.slot0 : 2 * (s.c0 + x)) * G + h;
+}
 
-// The heads h0, h0 + step, ... (kHeads of them at most, below `heads`) of the
-// split units, joined by one warp: head q is head q % G of unit q / G.  Lane c
-// holds the maximum and sum of the c-th of 32 CTAs, every lane 4 dims of the
-// accumulators; the accumulators of kAhead CTAs of all kHeads are requested
-// at a time.
-template <int kHeads, int kAhead>
-__device__ void join_heads(const DecodePagedArgs& a, int G, const SplitPlan& p,
-                           const SplitUnit (&split)[2], int heads, int h0, int step) {
+__device__ __forceinline__ void fma4(float4& acc, float f, const float4& v) {
+    acc.x = fmaf(f, v.x, acc.x);
+    acc.y = fmaf(f, v.y, acc.y);
+    acc.z = fmaf(f, v.z, acc.z);
+    acc.w = fmaf(f, v.w, acc.w);
+}
+
+__device__ __forceinline__ void write_joined(const DecodePagedArgs& a, int64_t row, const float4& o, float M,
+                                             float den) {
     const int lane = threadIdx.x & 31;
-    struct Head {
-        uint32_t i, c0, n, slot0, h;  // n = 0: none
-    } hd[kHeads];
-    uint32_t most = 0;
+    reinterpret_cast<float4*>(a.out + row * kD)[lane] =
+        den == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
+                   : make_float4(o.x / den, o.y / den, o.z / den, o.w / den);
+    if (a.lse && lane == 0) a.lse[row] = lse_of(M, den);
+}
+
+// Heads of units of at most kFew partials, by one warp, kHeads of them at a
+// time (n = 0: none): a lane has 4 dims and, by itself, all maxima and sums, so
+// nothing is exchanged and all loads are in flight together.
+constexpr int kFew = 4;
+template <int kHeads>
+__device__ void join_few(const DecodePagedArgs& a, int G, const SplitUnit (&s)[kHeads],
+                         const int (&h)[kHeads]) {
+    const int lane = threadIdx.x & 31;
+    float2 x[kHeads][kFew];
+    float4 v[kHeads][kFew];
 #pragma unroll
     for (int r = 0; r < kHeads; ++r) {
-        const int q = h0 + r * step;
-        const SplitUnit& s = split[q >= G && q < heads ? 1 : 0];
-        hd[r].i = s.i;
-        hd[r].h = q >= G ? q - G : q;
-        hd[r].c0 = cta_of_tile(p, s.tile0);
-        hd[r].n = q < heads && s.last ? cta_of_tile(p, s.tile0 + s.n_tiles - 1) - hd[r].c0 + 1 : 0;
-        hd[r].slot0 = part_slot(p, hd[r].c0, s.tile0);
-        most = max(most, hd[r].n);
+#pragma unroll
+        for (int y = 0; y < kFew; ++y) {
+            if (s[r].n == 0) continue;
+            const int64_t row = part_row(s[r], y, G, h[r]);
+            x[r][y] = __ldcg(a.part_ml + row);
+            v[r][y] = __ldcg(reinterpret_cast<const float4*>(a.part + row * kD) + lane);
+        }
     }
-    // Slot of the unit's x-th CTA; x past the last one repeats it.
-    auto slot = [&](const Head& d, uint32_t x) -> uint32_t {
-        x = min(x, d.n - 1);
-        return (x == 0 ? d.slot0 : 2 * (d.c0 + x)) * G + d.h;
-    };
-    float M[kHeads], den[kHeads];
-    float4 acc[kHeads];
 #pragma unroll
     for (int r = 0; r < kHeads; ++r) {
-        M[r] = -INFINITY;
-        den[r] = 0.f;
-        acc[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (s[r].n == 0) continue;
+        float M = x[r][0].x;
+#pragma unroll
+        for (int y = 1; y < kFew; ++y) M = fmaxf(M, x[r][y].x);
+        const float base = M == -INFINITY ? 0.f : M;
+        float den = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int y = 0; y < kFew; ++y) {
+            if (y >= static_cast<int>(s[r].n)) continue;
+            const float w = exp2f(x[r][y].x - base);
+            den = fmaf(w, x[r][y].y, den);
+            fma4(acc, w, v[r][y]);
+        }
+        write_joined(a, static_cast<int64_t>(s[r].i) * G + h[r], acc, M, den);
     }
+}
+
+// One head of a unit of any number of partials: lane c holds the maximum and
+// sum of the c-th of 32, every lane 4 dims; kAhead accumulators are requested
+// at a time.
+template <int kAhead>
+__device__ void join_many(const DecodePagedArgs& a, int G, const SplitUnit& s, int h) {
+    const int lane = threadIdx.x & 31;
+    float M = -INFINITY, den = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
-    for (uint32_t cb = 0; cb < most; cb += 32) {
-        float2 x[kHeads];
-        float w[kHeads];
-        float4 v[kHeads][kAhead];
+    for (uint32_t cb = 0; cb < s.n; cb += 32) {
+        const float2 x = __ldcg(a.part_ml + part_row(s, cb + lane, G, h));
+        float4 v[kAhead];
+        auto request = [&](uint32_t c) {
 #pragma unroll
-        for (int r = 0; r < kHeads; ++r)
-            if (hd[r].n) x[r] = __ldcg(a.part_ml + slot(hd[r], cb + lane));
-        auto request = [&](uint32_t b) {
-#pragma unroll
-            for (int r = 0; r < kHeads; ++r)
-#pragma unroll
-                for (int y = 0; y < kAhead; ++y)
-                    if (hd[r].n)
-                        v[r][y] = __ldcg(reinterpret_cast<const float4*>(
-                                             a.part + static_cast<int64_t>(slot(hd[r], b + y)) * kD) + lane);
+            for (int y = 0; y < kAhead; ++y)
+                v[y] = __ldcg(reinterpret_cast<const float4*>(
+                                  a.part + static_cast<int64_t>(part_row(s, c + y, G, h)) * kD) + lane);
         };
         request(cb);
+        const bool in = cb + lane < s.n;
+        float m = in ? x.x : -INFINITY;
 #pragma unroll
-        for (int r = 0; r < kHeads; ++r) {
-            const bool in = cb + lane < hd[r].n;
-            float m = in ? x[r].x : -INFINITY;
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        m = fmaxf(m, M);
+        const float base = m == -INFINITY ? 0.f : m;
+        const float f = exp2f(M - base);
+        const float w = in ? exp2f(x.x - base) : 0.f;
+        float l = in ? w * x.y : 0.f;
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            m = fmaxf(m, M[r]);
-            const float base = m == -INFINITY ? 0.f : m;
-            const float f = exp2f(M[r] - base);
-            w[r] = in ? exp2f(x[r].x - base) : 0.f;
-            float l = in ? w[r] * x[r].y : 0.f;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-            M[r] = m;
-            den[r] = fmaf(den[r], f, l);
-            acc[r] = make_float4(acc[r].x * f, acc[r].y * f, acc[r].z * f, acc[r].w * f);
-        }
+        for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+        M = m;
+        den = fmaf(den, f, l);
+        acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
 #pragma unroll 1
-        for (uint32_t b = 0; b < 32 && cb + b < most; b += kAhead) {
+        for (uint32_t b = 0; b < 32 && cb + b < s.n; b += kAhead) {
 #pragma unroll
-            for (int r = 0; r < kHeads; ++r) {
-#pragma unroll
-                for (int y = 0; y < kAhead; ++y) {
-                    const float g = __shfl_sync(0xffffffffu, w[r], b + y);
-                    if (cb + b + y >= hd[r].n) continue;
-                    acc[r].x = fmaf(g, v[r][y].x, acc[r].x);
-                    acc[r].y = fmaf(g, v[r][y].y, acc[r].y);
-                    acc[r].z = fmaf(g, v[r][y].z, acc[r].z);
-                    acc[r].w = fmaf(g, v[r][y].w, acc[r].w);
-                }
+            for (int y = 0; y < kAhead; ++y) {
+                const float g = __shfl_sync(0xffffffffu, w, b + y);
+                if (cb + b + y < s.n) fma4(acc, g, v[y]);
             }
-            if (b + kAhead < 32 && cb + b + kAhead < most) request(cb + b + kAhead);
+            if (b + kAhead < 32 && cb + b + kAhead < s.n) request(cb + b + kAhead);
         }
     }
-#pragma unroll
-    for (int r = 0; r < kHeads; ++r) {
-        if (!hd[r].n) continue;
-        const int64_t row = static_cast<int64_t>(hd[r].i) * G + hd[r].h;
-        const float d = den[r];
-        reinterpret_cast<float4*>(a.out + row * kD)[lane] =
-            d == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
-                     : make_float4(acc[r].x / d, acc[r].y / d, acc[r].z / d, acc[r].w / d);
-        if (a.lse && lane == 0) a.lse[row] = lse_of(M[r], d);
-    }
+    write_joined(a, static_cast<int64_t>(s.i) * G + h, acc, M, den);
 }
 
 // The partials of this CTA's n_split split units are written; of each unit the
 // CTA that arrives last joins the partials in CTA order,
-//   out = sum_c 2^(m_c - M) acc_c / sum_c 2^(m_c - M) l_c.
-// Called once, at the end, by the kWarps * 32 threads of named barrier kBar,
-// so the fence and the atomics are paid once.  What bounds it is the latency
-// of its loads: with many heads to join from few CTAs each a warp takes four
-// heads at a time, else two with more CTAs at a time.
-// (kAhead: as the kernel's registers allow.)
+//   out = sum_c 2^(m_c - M) acc_c / sum_c 2^(m_c - M) l_c,
+// a head a warp.  Called once, at the end, by the kWarps * 32 threads of named
+// barrier kBar, so the fence and the atomics are paid once.  Bound by the
+// latency of its loads.
 template <int kWarps, int kBar, int kAhead>
-__device__ void join_split_units(const DecodePagedArgs& a, int G, const SplitPlan& p, int n_split,
-                                 SplitUnit (&split)[2]) {
+__device__ void join_split_units(const DecodePagedArgs& a, int G, int n_split,
+                                 const SplitUnit& s0, const SplitUnit& s1) {
     __shared__ bool last[2];
     const int tid = threadIdx.x, warp = tid >> 5;
     wait_for_clear();
     named_sync(kBar, kWarps * 32);
-    uint32_t most = 0;
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-        if (x >= n_split) break;
-        const uint32_t more =
-            cta_of_tile(p, split[x].tile0 + split[x].n_tiles - 1) - cta_of_tile(p, split[x].tile0);
-        most = max(most, more + 1);
-        if (tid == x * 32) {
-            __threadfence();
-            last[x] = atomicAdd(a.counters + split[x].i, 1u) == more;
-            __threadfence();
-        }
+    if ((tid & 31) == 0 && warp < n_split) {
+        const uint32_t i = warp ? s1.i : s0.i, n = warp ? s1.n : s0.n;
+        __threadfence();
+        last[warp] = atomicAdd(a.counters + i, 1u) == n - 1;
+        __threadfence();
     }
     named_sync(kBar, kWarps * 32);
-    bool any = false;
+    // Head q: head q of the first unit that this CTA joins, or q - G of the other.
+    const bool j0 = n_split > 0 && last[0], j1 = n_split > 1 && last[1];
+    const int heads = (j0 ? G : 0) + (j1 ? G : 0);
+    constexpr int kAtOnce = kAhead / 4;
+#pragma unroll 1
+    for (int q0 = warp; q0 < heads; q0 += kWarps * kAtOnce) {
+        SplitUnit s[kAtOnce];
+        int h[kAtOnce];
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-        split[x].last = x < n_split && last[x];
-        any = any || split[x].last;
+        for (int r = 0; r < kAtOnce; ++r) {
+            const int q = q0 + r * kWarps;
+            s[r] = j0 && q < G ? s0 : s1;
+            h[r] = q >= G ? q - G : q;
+            if (q >= heads || s[r].n > kFew) s[r].n = 0;
+        }
+        join_few(a, G, s, h);
     }
-    if (!any) return;
-    const int heads = n_split * G;
-    if (most <= 4) {
 #pragma unroll 1
-        for (int q = warp; q < heads; q += 4 * kWarps) join_heads<4, 4>(a, G, p, split, heads, q, kWarps);
-    } else {
-#pragma unroll 1
-        for (int q = warp; q < heads; q += 2 * kWarps) join_heads<2, kAhead>(a, G, p, split, heads, q, kWarps);
+    for (int q = warp; q < heads; q += kWarps) {
+        const SplitUnit s = j0 && q < G ? s0 : s1;
+        if (s.n > kFew) join_many<kAhead>(a, G, s, q >= G ? q - G : q);
     }
 }
 
