@@ -552,6 +552,23 @@ PagedCache paged_cache(const int32_t* table, int64_t page_rows, int64_t pages_pe
     return pc;
 }
 
+// A bf16 pool of rows of 128 (a multiple of 8 of them) as {64 dims, 8 rows, 2
+// 64-dim halves, groups of 8 rows}: a box of whole groups lands as
+// [group][half][8 x 128 bytes], 128-byte swizzled, from contiguous rows.
+tri_status make_group_map(CUtensorMap* map, const void* pool, int64_t rows, int box_groups) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return TRI_ERR_CUDA;
+    const cuuint64_t dims[4] = {64, 8, 2, static_cast<cuuint64_t>(rows / 8)};
+    const cuuint64_t strides[3] = {256, 128, 2048};
+    const cuuint32_t box[4] = {64, 8, 2, static_cast<cuuint32_t>(box_groups)};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(pool), dims,
+                          strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? TRI_OK : TRI_ERR_CUDA;
+}
+
 struct DecodePagedWs {
     size_t counters, part, part_ml, total;
 };
@@ -1261,8 +1278,8 @@ tri_status tri_decode_attention_paged(const void* q, const void* k_pool, const v
     const int box = dt == TRI_BF16 ? decode_paged_box_rows(page_rows) : 0;
     CUtensorMap kmap, vmap;
     if (box) {
-        TRI_TRY(make_key_map(&kmap, k_pool, dt, n_pages * page_rows, box));
-        TRI_TRY(make_key_map(&vmap, v_pool, dt, n_pages * page_rows, box));
+        TRI_TRY(make_group_map(&kmap, k_pool, n_pages * page_rows, box / 8));
+        TRI_TRY(make_group_map(&vmap, v_pool, n_pages * page_rows, box / 8));
     }
     return cuda_status(box ? launch_decode_paged_tc(G, kmap, vmap, box, a, n_sm, s)
                            : launch_decode_paged_rows(dt, G, a, n_sm, s));

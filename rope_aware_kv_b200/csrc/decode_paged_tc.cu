@@ -1,9 +1,10 @@
 // decode_paged_tc.cu -- decode attention over a bf16 paged cache on the
 // tensor cores (the formulas stand in decode_paged.cu).
 //
-// A tile is 128 keys of one unit.  One warp brings its K and V rows in as TMA
-// boxes, each within one page, into a ring of kStages tiles (192 KB in
-// flight); four warps (one thread a key, then one thread a dim) work on it:
+// A tile is 128 keys of one unit; the tiles of a CTA are one stream over its
+// units.  One warp brings a tile's K and V rows in as TMA boxes, each within one
+// page, into a ring of kTcStages tiles (192 KB in flight), one warp issues the
+// products, and four warps (one thread a key, then one thread a dim) do the rest:
 //   S [128 keys x 16]  = K [128 x 128] Q^T             tcgen05, K rows as A;
 //                        the G <= 8 heads are columns, the rest zeros;
 //   weights            p = 2^(scale log2(e) s - m): the tile's maxima by a
@@ -16,11 +17,16 @@
 // few cycles more and the weights keep float32's precision.  Q and V are bf16
 // already, products are exact and sums are float32.  O of each tile is added
 // to float32 accumulators in registers with the rescale of the running
-// maximum, so nothing in tensor memory is rescaled.  S of the next tile is
-// issued together with O of this one.
+// maximum, so nothing in tensor memory is rescaled.
 //
-// Bound: K and V rows are read once (512 bytes a key), so HBM; the math of a
-// tile takes about half of the time that its 64 KB take to arrive.
+// S runs up to two tiles ahead (one over a change of unit), and O of a tile is
+// read after the next tile's weights, so no warp waits for a product that it
+// has just asked for; a unit's Q, row count and page entries are read while
+// the unit before it is worked on.
+//
+// Bound: K and V rows are read once (512 bytes a key), so HBM: 64 KB a tile
+// arrive in 1.5 us at an SM's share of it.  With the products issued by one of
+// the four warps a tile took 1.8 us, and 1792 units of 130 rows 96 us.
 #include "paged_core.cuh"
 #include "tri_launch.h"
 
@@ -28,22 +34,26 @@ namespace tri {
 
 constexpr int kTcStages = 3;
 constexpr int kTcMath = 128;               // threads of the math warps
-constexpr int kTcThreads = kTcMath + 32;   // and one loading warp
-constexpr int kTcHalf = kTcTile * 128;     // 64 dims of the tile's rows: 16 KB
-constexpr int kTcMat = 2 * kTcHalf;        // K or V of a tile
+constexpr int kTcThreads = kTcMath + 64;   // and a loading and an issuing warp
+constexpr int kTcMat = kTcTile * kD * 2;   // K or V of a tile: [8-row group][64-dim half][8 x 128 bytes]
+constexpr int kTcGroup = 2048;             // bytes of an 8-row group, and of
+constexpr int kTcHalf = 1024;              //   one half of it
 constexpr int kTcPRow = 64;                // bytes of a key's weights: 32 bf16
 
 struct __align__(1024) TcShared {
     unsigned char k[kTcStages][kTcMat];
     unsigned char v[kTcStages][kTcMat];
-    unsigned char q[2][16 * 128];       // [64-dim half][16 rows], swizzled
+    unsigned char q[2][2][16 * 128];    // [unit in turn][64-dim half][16 rows], swizzled
     unsigned char p[kTcTile * kTcPRow]; // [key][32 columns], swizzled
-    float wmax[4][8];
+    float wmax[2][4][8];                // [tile in turn][warp][head]
     float wsum[4][8];
     uint64_t k_full[kTcStages], k_empty[kTcStages], v_full[kTcStages], v_empty[kTcStages];
     uint64_t s_full[2], o_full;
+    uint64_t p_full;                    // Q of the first tile; then P of a tile (and Q of the next)
+    uint32_t q_next;                    // bit 0: Q of the next tile; bit 1: the one behind it has it too
     uint32_t tmem;
-    int abort;
+    int abort[2];                       // [tile in turn]: a wait gave up before the tile's barrier
+    int failed;
 };
 
 // ---- tcgen05 ----
@@ -101,26 +111,25 @@ constexpr uint32_t tc_idesc(uint32_t n, bool a_m_major, bool b_n_major) {
 }
 
 // S = K Q^T: both operands K-major (dims contiguous) in 128-byte rows, 8-row
-// groups 1024 bytes apart; 16 dims are 32 bytes.
-__device__ __forceinline__ void issue_scores(TcShared& sm, int stage, uint32_t tmem) {
+// groups 2048 (K) and 1024 (Q) bytes apart; 16 dims are 32 bytes.  (A
+// descriptor's address counts 16-byte units in its lowest bits.)
+__device__ __forceinline__ void issue_scores(uint64_t k, uint64_t q, uint32_t tmem) {
     constexpr uint32_t idesc = tc_idesc(16, false, false);
 #pragma unroll
     for (int x = 0; x < kD / 16; ++x) {
         const int half = x >> 2, off = (x & 3) * 32;
-        tc_mma(tmem, tc_desc(sm.k[stage] + half * kTcHalf + off, 16, 1024, 2),
-               tc_desc(sm.q[half] + off, 16, 1024, 2), idesc, x > 0);
+        tc_mma(tmem, k + ((half * kTcHalf + off) >> 4), q + ((half * 2048 + off) >> 4), idesc, x > 0);
     }
 }
 
-// O = V^T P: V's 64-dim halves (A, M contiguous) kTcHalf bytes apart, 8-key
-// groups 1024 bytes apart; P (B, N contiguous) 64-byte keys, 8-key groups 512
+// O = V^T P: V (A, M contiguous) with its 64-dim halves 1024 and its 8-key
+// groups 2048 bytes apart; P (B, N contiguous) 64-byte keys, 8-key groups 512
 // bytes apart; 16 keys a step.
-__device__ __forceinline__ void issue_values(TcShared& sm, int stage, uint32_t tmem) {
+__device__ __forceinline__ void issue_values(uint64_t v, uint64_t p, uint32_t tmem) {
     constexpr uint32_t idesc = tc_idesc(32, true, true);
 #pragma unroll
     for (int x = 0; x < kTcTile / 16; ++x)
-        tc_mma(tmem, tc_desc(sm.v[stage] + x * 2048, kTcHalf, 1024, 2),
-               tc_desc(sm.p + x * 16 * kTcPRow, 16, 512, 4), idesc, x > 0);
+        tc_mma(tmem, v + ((x * 2 * kTcGroup) >> 4), p + ((x * 16 * kTcPRow) >> 4), idesc, x > 0);
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
@@ -128,16 +137,100 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return *reinterpret_cast<const uint32_t*>(&x);
 }
 
+// A box of the 4-D view {64 dims, 8 rows, 2 halves, groups} of a pool: whole
+// groups, each 2048 contiguous bytes here and there.
+__device__ __forceinline__ void tma_load_groups(void* dst, const CUtensorMap* map, uint64_t* bar,
+                                                int32_t group, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%3, %3, %3, %4}], [%2], %5;" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(0), "r"(group), "l"(policy)
+        : "memory");
+}
+
+// Maxima or sums of 8 values over a warp by a transposing butterfly: lane x
+// gets value x >> 2.
+template <typename Op>
+__device__ __forceinline__ float reduce8(float (&x)[8], Op op) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int q = 0; q < 3; ++q) {
+        const int o = 16 >> q, c = 4 >> q;
+        const bool up = lane & o;
+#pragma unroll
+        for (int h = 0; h < c; ++h) {
+            const float keep = up ? x[h + c] : x[h];
+            const float give = up ? x[h] : x[h + c];
+            x[h] = op(keep, __shfl_xor_sync(0xffffffffu, give, o));
+        }
+    }
+    x[0] = op(x[0], __shfl_xor_sync(0xffffffffu, x[0], 2));
+    return op(x[0], __shfl_xor_sync(0xffffffffu, x[0], 1));
+}
+
+// j / page_rows for j < 2^31 by a multiplication: with 2^l >= d > 2^(l-1) and
+// m = floor(2^(31+l) / d) + 1, the product m d exceeds 2^(31+l) by at most 2^l,
+// so floor(j m / 2^(31+l)) is exact.  (d >= 8 here.)
+struct PageDivide {
+    uint32_t m, shift, rows;
+    __device__ __forceinline__ uint32_t slot(uint32_t j) const { return __umulhi(j, m) >> shift; }
+};
+
+// A unit of the CTA's range, and the row counts of the two units behind it
+// (read ahead).
+struct TcUnit {
+    uint32_t i, tile0, n, n_tiles;
+    uint32_t t1;           // its tiles in the range end here
+    uint32_t n1, n2;
+    const int32_t* pages;  // its page table row
+
+    __device__ static uint32_t rows_of(const DecodePagedArgs& a, uint32_t i) {
+        if (i >= static_cast<uint32_t>(a.sl.n)) return 0;
+        return clamp_nvalid(a.n_valid, slice_unit(a.sl, i), a.pc.per_unit * a.pc.rows, nullptr);
+    }
+    __device__ void set(const DecodePagedArgs& a, const SplitPlan& p, uint32_t rows) {
+        n = rows;
+        n_tiles = (n + kTcTile - 1) / kTcTile;
+        t1 = min(tile0 + n_tiles, p.end);
+        pages = a.pc.table + slice_unit(a.sl, i) * a.pc.per_unit;
+    }
+    __device__ void first(const DecodePagedArgs& a, const SplitPlan& p) {
+        i = p.unit;
+        tile0 = p.tile0;
+        set(a, p, p.rows);
+        n1 = rows_of(a, i + 1);
+        n2 = rows_of(a, i + 2);
+    }
+    // The next unit with rows (there is one while t1 < p.end).
+    __device__ TcUnit next(const DecodePagedArgs& a, const SplitPlan& p) const {
+        TcUnit x;
+        x.tile0 = tile0 + n_tiles;
+        x.i = i + 1;
+        x.n1 = n2;
+        uint32_t rows = n1;
+        while (rows == 0 && x.i + 1 < static_cast<uint32_t>(a.sl.n)) {
+            rows = x.n1;
+            ++x.i;
+            x.n1 = rows_of(a, x.i + 1);
+        }
+        x.i = min(x.i, static_cast<uint32_t>(a.sl.n) - 1);
+        x.set(a, p, rows);
+        x.n2 = rows_of(a, x.i + 2);
+        return x;
+    }
+    // Page entry of row j, -1 past the last row.
+    __device__ int32_t page(const PageDivide& d, uint32_t j) const { return j < n ? pages[d.slot(j)] : -1; }
+};
+
 template <int G>
 __global__ void __launch_bounds__(kTcThreads, 1)
 decode_paged_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                        const __grid_constant__ CUtensorMap vmap, const int box_rows,
-                       const DecodePagedArgs a) {
+                       const PageDivide divide, const DecodePagedArgs a) {
     extern __shared__ unsigned char smem_raw[];
     TcShared& sm = *reinterpret_cast<TcShared*>(
         smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023));
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int64_t cap = a.pc.per_unit * a.pc.rows;
     if (tid == kTcMath) {
         for (int i = 0; i < kTcStages; ++i) {
             mbar_init(&sm.k_full[i], 1);
@@ -148,7 +241,8 @@ decode_paged_tc_kernel(const __grid_constant__ CUtensorMap kmap,
         mbar_init(&sm.s_full[0], 1);
         mbar_init(&sm.s_full[1], 1);
         mbar_init(&sm.o_full, 1);
-        sm.abort = 0;
+        mbar_init(&sm.p_full, kTcMath / 32);
+        sm.abort[0] = sm.abort[1] = sm.failed = 0;
         fence_barrier_init();
         prefetch_tensormap(&kmap);
         prefetch_tensormap(&vmap);
@@ -156,249 +250,288 @@ decode_paged_tc_kernel(const __grid_constant__ CUtensorMap kmap,
     const SplitPlan p = plan_split<kTcThreads>(a, kTcTile, 1);  // (synchronises the CTA)
     // The loading warp goes on while the others get their tensor memory.
     uint32_t tmem = 0;
-    if (warp < kTcMath / 32) {
+    if (warp != kTcMath / 32) {
         if (warp == 0) tc_alloc(&sm.tmem, 64);
         // Columns 24 .. 31 of the weights stay zeros.
-        *reinterpret_cast<uint4*>(sm.p + tid * kTcPRow + ((3 ^ ((tid >> 1) & 3)) * 16)) =
-            make_uint4(0, 0, 0, 0);
+        if (tid < kTcMath)
+            *reinterpret_cast<uint4*>(sm.p + tid * kTcPRow + ((3 ^ ((tid >> 1) & 3)) * 16)) =
+                make_uint4(0, 0, 0, 0);
         tc_fence_before();
-        named_sync(1, kTcMath);
+        named_sync(2, kTcMath + 32);
         tc_fence_after();
         tmem = sm.tmem;
     }
+    const uint32_t s_cols = tmem, o_cols = tmem + 32;
+    const uint32_t n_it = p.end - p.begin;  // tiles of this CTA
+    auto aborted = [&] {
+        return (*reinterpret_cast<volatile int*>(&sm.abort[0]) | *reinterpret_cast<volatile int*>(&sm.abort[1])) != 0;
+    };
 
-    uint32_t it = 0;  // tiles of this CTA so far
-    uint32_t t = p.begin, i = p.unit, tile0 = p.tile0;
     if (warp == kTcMath / 32) {
         // ---- the loading warp: lane b brings box b ----
         const int n_boxes = kTcTile / box_rows;
         const uint64_t pol = policy_evict_first();
-        for (; t < p.end; ++i) {
-            const int64_t u = slice_unit(a.sl, i);
-            const uint32_t n = i == p.unit ? p.rows : clamp_nvalid(a.n_valid, u, cap, nullptr);
-            const uint32_t n_tiles = static_cast<uint32_t>(n + kTcTile - 1) / kTcTile;
-            if (n_tiles == 0) continue;
-            const uint32_t t1 = min(tile0 + n_tiles, p.end);
-            for (; t < t1; ++t, ++it) {
-                const int stage = it % kTcStages;
-                const uint32_t parity = ((it / kTcStages) & 1) ^ 1;
-                const int64_t j = static_cast<int64_t>(t - tile0) * kTcTile + lane * box_rows;
-                int64_t row = lane < n_boxes && j < cap ? paged_row(a.pc, u, j) : -1;
-                if (lane < n_boxes && j < n && row < 0) {
-                    wait_for_clear();
-                    raise_flag(a.flag, TRI_FLAG_INDEX_RANGE);
-                }
-                if (j >= n) row = -1;
-                const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, row >= 0)) * box_rows * 256;
-                const int off = lane * box_rows * 128;
-                bool ok = mbar_wait(&sm.k_empty[stage], parity, a.flag);
-                ok = __all_sync(0xffffffffu, ok && !*reinterpret_cast<volatile int*>(&sm.abort));
-                if (!ok) break;
-                if (lane == 0) mbar_arrive_expect_tx(&sm.k_full[stage], bytes);
-                __syncwarp();
-                if (row >= 0) {
-                    const int32_t y = static_cast<int32_t>(row);
-                    tma_load_2d_hint(sm.k[stage] + off, &kmap, &sm.k_full[stage], 0, y, pol);
-                    tma_load_2d_hint(sm.k[stage] + kTcHalf + off, &kmap, &sm.k_full[stage], 64, y, pol);
-                }
-                ok = mbar_wait(&sm.v_empty[stage], parity, a.flag);
-                ok = __all_sync(0xffffffffu, ok);
-                if (lane == 0) mbar_arrive_expect_tx(&sm.v_full[stage], ok ? bytes : 0);
-                __syncwarp();
-                if (ok && row >= 0) {
-                    const int32_t y = static_cast<int32_t>(row);
-                    tma_load_2d_hint(sm.v[stage] + off, &vmap, &sm.v_full[stage], 0, y, pol);
-                    tma_load_2d_hint(sm.v[stage] + kTcHalf + off, &vmap, &sm.v_full[stage], 64, y, pol);
-                }
+        TcUnit cur = {};
+        // Page entry of this lane's box of tile t (read a tile ahead).
+        auto look_up = [&](const TcUnit& w, uint32_t t) -> int32_t {
+            return lane < n_boxes ? w.page(divide, (t - w.tile0) * kTcTile + lane * box_rows) : -1;
+        };
+        int32_t page = -1;
+        if (n_it) {
+            cur.first(a, p);
+            page = look_up(cur, p.begin);
+        }
+        uint32_t it = 0;
+        for (; it < n_it; ++it) {
+            const uint32_t t = p.begin + it;
+            const int stage = it % kTcStages;
+            const uint32_t parity = ((it / kTcStages) & 1) ^ 1;
+            const uint32_t j = (t - cur.tile0) * kTcTile + lane * box_rows;
+            const bool wanted = lane < n_boxes && j < cur.n;
+            if (t + 1 == cur.t1 && it + 1 < n_it) cur = cur.next(a, p);
+            const int32_t page_next = it + 1 < n_it ? look_up(cur, t + 1) : -1;
+            const bool load = page >= 0 && page < a.pc.n_pages;
+            if (wanted && !load) {
+                wait_for_clear();
+                raise_flag(a.flag, TRI_FLAG_INDEX_RANGE);
             }
-            if (t < t1) break;  // gave up
-            tile0 += n_tiles;
+            const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, load)) * box_rows * 256;
+            const int off = lane * box_rows * 256;
+            const uint32_t in_page = j - divide.slot(j) * divide.rows;
+            const int32_t group = static_cast<int32_t>((static_cast<int64_t>(page) * divide.rows + in_page) >> 3);
+            bool ok = mbar_wait(&sm.k_empty[stage], parity, a.flag);
+            ok = __all_sync(0xffffffffu, ok && !aborted());
+            if (!ok) break;
+            if (lane == 0) mbar_arrive_expect_tx(&sm.k_full[stage], bytes);
+            __syncwarp();
+            if (load) tma_load_groups(sm.k[stage] + off, &kmap, &sm.k_full[stage], group, pol);
+            ok = mbar_wait(&sm.v_empty[stage], parity, a.flag);
+            ok = __all_sync(0xffffffffu, ok);
+            if (lane == 0) mbar_arrive_expect_tx(&sm.v_full[stage], ok ? bytes : 0);
+            __syncwarp();
+            if (ok && load) tma_load_groups(sm.v[stage] + off, &vmap, &sm.v_full[stage], group, pol);
+            page = page_next;
         }
         // Nothing of this warp is in flight when the CTA ends.
         for (uint32_t x = it < kTcStages ? 0 : it - kTcStages; x < it; ++x) {
             mbar_wait(&sm.k_full[x % kTcStages], (x / kTcStages) & 1, a.flag);
             mbar_wait(&sm.v_full[x % kTcStages], (x / kTcStages) & 1, a.flag);
         }
+    } else if (warp == kTcMath / 32 + 1) {
+        // ---- the issuing warp: one thread ----
+        if (lane == 0 && n_it) {
+            const uint64_t kd = tc_desc(sm.k, 16, kTcGroup, 2), qd = tc_desc(sm.q, 16, 1024, 2);
+            const uint64_t vd = tc_desc(sm.v, kTcHalf, kTcGroup, 2), pd = tc_desc(sm.p, 16, 512, 4);
+            uint32_t asked = 0;  // scores issued: of tiles 0 .. asked - 1
+            auto scores = [&](uint32_t qb) {
+                const uint32_t x = asked++, stage = x % kTcStages;
+                if (!mbar_wait(&sm.k_full[stage], (x / kTcStages) & 1, a.flag)) return false;
+                tc_fence_after();
+                issue_scores(kd + stage * (kTcMat >> 4), qd + qb * (4096 >> 4), s_cols + (x & 1) * 16);
+                tc_commit(&sm.s_full[x & 1]);
+                tc_commit(&sm.k_empty[stage]);
+                return true;
+            };
+            bool ok = mbar_wait(&sm.p_full, 0, a.flag);
+            uint32_t w = *reinterpret_cast<volatile uint32_t*>(&sm.q_next);
+            ok = ok && scores(w & 1);
+            if (ok && (w & 2)) ok = scores(w & 1);
+            for (uint32_t it = 0; ok && it < n_it; ++it) {
+                const int stage = it % kTcStages;
+                ok = mbar_wait(&sm.p_full, (it + 1) & 1, a.flag) &&
+                     mbar_wait(&sm.v_full[stage], (it / kTcStages) & 1, a.flag);
+                if (!ok) break;
+                w = *reinterpret_cast<volatile uint32_t*>(&sm.q_next);
+                tc_fence_after();
+                issue_values(vd + stage * (kTcMat >> 4), pd, o_cols);
+                tc_commit(&sm.o_full);
+                tc_commit(&sm.v_empty[stage]);
+                if (asked == it + 1 && asked < n_it) ok = scores(w & 1);
+                if (ok && asked == it + 2 && (w & 2)) ok = scores(w & 1);
+            }
+        }
+        __syncwarp();
     } else {
         const uint32_t lanes = static_cast<uint32_t>(warp) * 32 << 16;  // this warp's TMEM lanes
-        const uint32_t s_cols = tmem, o_cols = tmem + 32;
-        const uint32_t page_rows = static_cast<uint32_t>(a.pc.rows);
         SplitUnit split0 = {}, split1 = {};
         int n_split = 0;
+        uint32_t qb = 0;
         bool ok = true;
-        while (t < p.end) {
-            const int64_t u = slice_unit(a.sl, i);
-            const uint32_t n = i == p.unit ? p.rows : clamp_nvalid(a.n_valid, u, cap, nullptr);
-            const uint32_t n_tiles = static_cast<uint32_t>(n + kTcTile - 1) / kTcTile;
-            if (n_tiles == 0) {
-                ++i;
-                continue;
-            }
-            const uint32_t t1 = min(tile0 + n_tiles, p.end);
-            const bool from_start = t == tile0;
-            // ---- Q, rows >= G zero; 16-byte chunk c of a 128-byte row r lies at c ^ (r & 7) ----
-            for (int e = tid; e < 16 * 16; e += kTcMath) {
-                const int r = e >> 4, c = e & 15;
-                uint4 x = make_uint4(0, 0, 0, 0);
+        float m[G], l[G], acc[G], al[G];
+        // Q of unit i, rows >= G zero: chunks tid and tid + 128 of its 16 x 16;
+        // 16-byte chunk c of a 128-byte row r lies at c ^ (r & 7).
+        uint4 qx[2];
+        auto read_q = [&](uint32_t i) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const int e = tid + x * kTcMath, r = e >> 4, c = e & 15;
+                qx[x] = make_uint4(0, 0, 0, 0);
                 if (r < G)
-                    x = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
-                                                             (static_cast<int64_t>(i) * G + r) * kD) +
-                              c);
-                *reinterpret_cast<uint4*>(sm.q[c >> 3] + r * 128 + ((c & 7) ^ (r & 7)) * 16) = x;
+                    qx[x] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
+                                                                 (static_cast<int64_t>(i) * G + r) * kD) +
+                                  c);
             }
-            float m[G], l[G], acc[G];
+        };
+        auto store_q = [&](uint32_t b) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const int e = tid + x * kTcMath, r = e >> 4, c = e & 15;
+                *reinterpret_cast<uint4*>(sm.q[b][c >> 3] + r * 128 + ((c & 7) ^ (r & 7)) * 16) = qx[x];
+            }
+        };
+        // What this warp wrote (and read of tensor memory) is handed to the
+        // issuing warp.
+        auto hand_over = [&] {
+            fence_proxy_async();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.p_full);
+        };
+        // O of the tile x that was last handed over, into the accumulators.
+        auto take_values = [&](uint32_t x) {
+            ok = mbar_wait(&sm.o_full, x & 1, a.flag) && ok;
+            tc_fence_after();
+            float o1[8], o2[8], o3[8];
+            tc_load8(o_cols + lanes, o1);
+            tc_load8(o_cols + 8 + lanes, o2);
+            tc_load8(o_cols + 16 + lanes, o3);
+            tc_load_wait();
 #pragma unroll
             for (int h = 0; h < G; ++h) {
-                m[h] = -INFINITY;
-                l[h] = acc[h] = 0.f;
+                // An infinite value times a term of zero is no part of the sum.
+                const float rest = isfinite(o1[h]) ? o2[h] + o3[h] : 0.f;
+                acc[h] = fmaf(acc[h], al[h], o1[h] + rest);
             }
-            fence_proxy_async();
+        };
+        TcUnit cur = {};
+        int32_t page = -1;  // entry of this thread's key (read a tile ahead)
+        if (n_it) {
+            read_q(p.unit);
+            cur.first(a, p);
+            page = cur.page(divide, (p.begin - cur.tile0) * kTcTile + tid);
+            store_q(0);
+            if (tid == 0) sm.q_next = p.begin + 1 < cur.t1 ? 2 : 0;
+            hand_over();
+        }
+        bool begins = true;  // the tile is its unit's first in the range
+        for (uint32_t it = 0; it < n_it; ++it) {
+            const uint32_t t = p.begin + it;
+            const int stage = it % kTcStages;
+            const bool ends = t + 1 == cur.t1, more = it + 1 < n_it;
+            const bool valid = page >= 0 && page < a.pc.n_pages;
+            TcUnit nxt = cur;
+            if (ends && more) {
+                nxt = cur.next(a, p);
+                read_q(nxt.i);
+            }
+            page = more ? nxt.page(divide, (t + 1 - nxt.tile0) * kTcTile + tid) : -1;
+            ok = mbar_wait(&sm.s_full[it & 1], (it >> 1) & 1, a.flag) && ok;
+            tc_fence_after();
+            float s[8];
+            tc_load8(s_cols + (it & 1) * 16 + lanes, s);
+            tc_load_wait();
+            // ---- maxima of the warp's 32 keys ----
+            float x[8];
+#pragma unroll
+            for (int h = 0; h < 8; ++h) x[h] = h < G && valid ? s[h] * a.scale_log2 : -INFINITY;
+            const float wm = reduce8(x, [](float u, float v) { return fmaxf(u, v); });
+            if ((lane & 3) == 0) sm.wmax[it & 1][warp][lane >> 2] = wm;
+            if (!ok) *reinterpret_cast<volatile int*>(&sm.abort[it & 1]) = 1;
             named_sync(1, kTcMath);
-            auto start_scores = [&](uint32_t x) {
-                ok = mbar_wait(&sm.k_full[x % kTcStages], (x / kTcStages) & 1, a.flag) && ok;
-                tc_fence_after();
-                issue_scores(sm, x % kTcStages, s_cols + (x & 1) * 16);
-                tc_commit(&sm.s_full[x & 1]);
-                tc_commit(&sm.k_empty[x % kTcStages]);
-            };
-            if (tid == 0) start_scores(it);
-            // Whether this thread's key of tile x has a row (looked up a tile ahead).
-            auto has_row = [&](uint32_t x) {
-                const uint32_t j = (x - tile0) * kTcTile + tid;
-                return x < t1 && j < n && page_of(a.pc, u, j / page_rows) >= 0;
-            };
-            bool valid = has_row(t);
-            for (; t < t1; ++t, ++it) {
-                const int stage = it % kTcStages;
-                const uint32_t parity = (it / kTcStages) & 1;
-                const bool valid_next = has_row(t + 1);
-                ok = mbar_wait(&sm.s_full[it & 1], (it >> 1) & 1, a.flag) && ok;
-                tc_fence_after();
-                float s[8];
-                tc_load8(s_cols + (it & 1) * 16 + lanes, s);
-                tc_load_wait();
-                tc_fence_before();
-                // ---- maxima of the warp's 32 keys: 8 values, halved 3 times ----
-                float x[8];
-#pragma unroll
-                for (int h = 0; h < 8; ++h) {
-                    x[h] = h < G && valid ? s[h] * a.scale_log2 : -INFINITY;
-                }
-#pragma unroll
-                for (int q = 0; q < 3; ++q) {
-                    const int o = 16 >> q, c = 4 >> q;
-                    const bool up = lane & o;
-#pragma unroll
-                    for (int h = 0; h < c; ++h) {
-                        const float keep = up ? x[h + c] : x[h];
-                        const float give = up ? x[h] : x[h + c];
-                        x[h] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, give, o));
-                    }
-                }
-                x[0] = fmaxf(x[0], __shfl_xor_sync(0xffffffffu, x[0], 2));
-                x[0] = fmaxf(x[0], __shfl_xor_sync(0xffffffffu, x[0], 1));
-                if ((lane & 3) == 0) sm.wmax[warp][lane >> 2] = x[0];
-                const bool part_tile = !__all_sync(0xffffffffu, valid);
-                if (part_tile) ok = mbar_wait(&sm.v_full[stage], parity, a.flag) && ok;
-                if (!ok) *reinterpret_cast<volatile int*>(&sm.abort) = 1;
-                named_sync(1, kTcMath);
-                if (*reinterpret_cast<volatile int*>(&sm.abort)) break;
-                float al[G];
+            if (*reinterpret_cast<volatile int*>(&sm.abort[it & 1])) {
+                ok = false;
+                break;
+            }
+            if (begins) {
 #pragma unroll
                 for (int h = 0; h < G; ++h) {
-                    const float mt = fmaxf(fmaxf(sm.wmax[0][h], sm.wmax[1][h]),
-                                           fmaxf(sm.wmax[2][h], sm.wmax[3][h]));
-                    const float m_new = fmaxf(m[h], mt);
-                    const float base = m_new == -INFINITY ? 0.f : m_new;
-                    al[h] = exp2f(m[h] - base);
-                    // (one rounding of the small difference, not of the large product)
-                    const float w = valid ? exp2f(fmaf(s[h], a.scale_log2, -base)) : 0.f;
-                    l[h] = fmaf(l[h], al[h], w);
-                    m[h] = m_new;
-                    s[h] = w;
+                    m[h] = -INFINITY;
+                    l[h] = acc[h] = 0.f;
                 }
-                // ---- P: three bf16 terms; chunk c of key t's 64 bytes lies at c ^ ((t >> 1) & 3) ----
-                unsigned char* prow = sm.p + tid * kTcPRow;
-                const int sw = (tid >> 1) & 3;
+            }
+            float al_now[G];
 #pragma unroll
-                for (int term = 0; term < 3; ++term) {
-                    uint32_t w[4];
+            for (int h = 0; h < G; ++h) {
+                const float mt = fmaxf(fmaxf(sm.wmax[it & 1][0][h], sm.wmax[it & 1][1][h]),
+                                       fmaxf(sm.wmax[it & 1][2][h], sm.wmax[it & 1][3][h]));
+                const float m_new = fmaxf(m[h], mt);
+                const float base = m_new == -INFINITY ? 0.f : m_new;
+                al_now[h] = exp2f(m[h] - base);
+                // (one rounding of the small difference, not of the large product)
+                const float w = valid ? exp2f(fmaf(s[h], a.scale_log2, -base)) : 0.f;
+                l[h] = fmaf(l[h], al_now[h], w);
+                m[h] = m_new;
+                s[h] = w;
+            }
+            // The tile before this one; from here on P may be written again.
+            if (!begins) take_values(it - 1);
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const float lo = 2 * c < G ? s[2 * c] : 0.f;
-                        const float hi = 2 * c + 1 < G ? s[2 * c + 1] : 0.f;
-                        w[c] = pack_bf16(lo, hi);
-                        if (2 * c < G) s[2 * c] = lo - bf16_lo(w[c]);
-                        if (2 * c + 1 < G) s[2 * c + 1] = hi - bf16_hi(w[c]);
-                    }
-                    *reinterpret_cast<uint4*>(prow + ((term ^ sw) * 16)) = make_uint4(w[0], w[1], w[2], w[3]);
+            for (int h = 0; h < G; ++h) al[h] = al_now[h];
+            // ---- P: three bf16 terms; chunk c of key t's 64 bytes lies at c ^ ((t >> 1) & 3) ----
+            unsigned char* prow = sm.p + tid * kTcPRow;
+            const int sw = (tid >> 1) & 3;
+#pragma unroll
+            for (int term = 0; term < 3; ++term) {
+                uint32_t w[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const float lo = 2 * c < G ? s[2 * c] : 0.f;
+                    const float hi = 2 * c + 1 < G ? s[2 * c + 1] : 0.f;
+                    w[c] = pack_bf16(lo, hi);
+                    if (2 * c < G) s[2 * c] = lo - bf16_lo(w[c]);
+                    if (2 * c + 1 < G) s[2 * c + 1] = hi - bf16_hi(w[c]);
                 }
-                // Rows that carry no weight hold anything: zeros, since 0 * inf is not 0.
+                *reinterpret_cast<uint4*>(prow + ((term ^ sw) * 16)) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            // Rows that carry no weight hold anything: zeros, since 0 * inf is
+            // not 0.  (The chunks in an order that spreads the lanes' banks.)
+            if (!__all_sync(0xffffffffu, valid)) {
+                ok = mbar_wait(&sm.v_full[stage], (it / kTcStages) & 1, a.flag) && ok;
                 if (!valid) {
 #pragma unroll
                     for (int c = 0; c < 16; ++c)
-                        *reinterpret_cast<uint4*>(sm.v[stage] + (c >> 3) * kTcHalf + tid * 128 +
-                                                  (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+                        *reinterpret_cast<uint4*>(sm.v[stage] + (tid >> 3) * kTcGroup + (c >> 3) * kTcHalf +
+                                                  (tid & 7) * 128 + ((c + tid) & 7) * 16) = make_uint4(0, 0, 0, 0);
                 }
-                fence_proxy_async();
-                named_sync(1, kTcMath);
-                if (tid == 0) {
-                    ok = mbar_wait(&sm.v_full[stage], parity, a.flag) && ok;
-                    tc_fence_after();
-                    issue_values(sm, stage, o_cols);
-                    tc_commit(&sm.o_full);
-                    tc_commit(&sm.v_empty[stage]);
-                    if (t + 1 < t1) start_scores(it + 1);
-                }
-                __syncwarp();
-                ok = mbar_wait(&sm.o_full, it & 1, a.flag) && ok;
-                tc_fence_after();
-                float o1[8], o2[8], o3[8];
-                tc_load8(o_cols + lanes, o1);
-                tc_load8(o_cols + 8 + lanes, o2);
-                tc_load8(o_cols + 16 + lanes, o3);
-                tc_load_wait();
-                tc_fence_before();
-#pragma unroll
-                for (int h = 0; h < G; ++h) {
-                    // An infinite value times a term of zero is no part of the sum.
-                    const float rest = isfinite(o1[h]) ? o2[h] + o3[h] : 0.f;
-                    acc[h] = fmaf(acc[h], al[h], o1[h] + rest);
-                }
-                valid = valid_next;
             }
-            // ---- the unit's sums over the keys ----
-#pragma unroll
-            for (int h = 0; h < G; ++h) {
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], o);
-                if (lane == 0) sm.wsum[warp][h] = l[h];
+            if (ends && more) {
+                qb ^= 1;
+                store_q(qb);
             }
-            if (!ok) *reinterpret_cast<volatile int*>(&sm.abort) = 1;
+            if (tid == 0) sm.q_next = qb | (t + 2 < nxt.t1 ? 2u : 0u);
+            hand_over();
+            begins = ends;
+            if (!ends) continue;
+            // ---- the unit's sums over the keys, and its results ----
+            take_values(it);
+#pragma unroll
+            for (int h = 0; h < 8; ++h) x[h] = h < G ? l[h] : 0.f;
+            const float ws = reduce8(x, [](float u, float v) { return u + v; });
+            if ((lane & 3) == 0) sm.wsum[warp][lane >> 2] = ws;
             named_sync(1, kTcMath);
-            if (*reinterpret_cast<volatile int*>(&sm.abort)) break;
-            const bool whole = from_start && t1 == tile0 + n_tiles;
-            const uint32_t slot = part_slot(p, blockIdx.x, tile0);
+            const bool whole = cur.tile0 >= p.begin && cur.t1 == cur.tile0 + cur.n_tiles;
+            const uint32_t slot = part_slot(p, blockIdx.x, cur.tile0);
 #pragma unroll
             for (int h = 0; h < G; ++h) {
                 const float den = (sm.wsum[0][h] + sm.wsum[1][h]) + (sm.wsum[2][h] + sm.wsum[3][h]);
                 if (whole) {
-                    a.out[(static_cast<int64_t>(i) * G + h) * kD + tid] = den == 0.f ? 0.f : acc[h] / den;
-                    if (a.lse && tid == 0) a.lse[static_cast<int64_t>(i) * G + h] = lse_of(m[h], den);
+                    const int64_t row = static_cast<int64_t>(cur.i) * G + h;
+                    a.out[row * kD + tid] = den == 0.f ? 0.f : acc[h] / den;
+                    if (a.lse && tid == 0) a.lse[row] = lse_of(m[h], den);
                 } else {
                     a.part[(slot * G + h) * kD + tid] = acc[h];
                     if (tid == 0) a.part_ml[slot * G + h] = make_float2(m[h], den);
                 }
             }
             if (!whole) {
-                split1 = split_unit(p, i, tile0, n_tiles);
+                split1 = split_unit(p, cur.i, cur.tile0, cur.n_tiles);
                 if (n_split++ == 0) split0 = split1;
             }
-            named_sync(1, kTcMath);  // wsum and Q are rewritten by the next unit
-            tile0 += n_tiles;
-            ++i;
+            cur = nxt;
         }
-        if (!*reinterpret_cast<volatile int*>(&sm.abort))
+        if (!ok) *reinterpret_cast<volatile int*>(&sm.failed) = 1;
+        named_sync(1, kTcMath);
+        if (!*reinterpret_cast<volatile int*>(&sm.failed))
             join_split_units<kTcMath / 32, 1, 16>(a, G, n_split, split0, split1);
     }
     wait_for_clear();
@@ -428,7 +561,13 @@ static cudaError_t launch_tc(const CUtensorMap& kmap, const CUtensorMap& vmap, i
     if (e != cudaSuccess) return e;
     e = launch_decode_paged_clear(a, s);
     if (e != cudaSuccess) return e;
-    e = launch_early(fn, decode_paged_ctas(n_sm), kTcThreads, smem, s, kmap, vmap, box_rows, a);
+    PageDivide d;
+    d.rows = static_cast<uint32_t>(a.pc.rows);
+    uint32_t l = 3;
+    while ((1ull << l) < d.rows) ++l;
+    d.m = static_cast<uint32_t>((1ull << (31 + l)) / d.rows + 1);
+    d.shift = l - 1;
+    e = launch_early(fn, decode_paged_ctas(n_sm), kTcThreads, smem, s, kmap, vmap, box_rows, d, a);
     if (e == cudaSuccess) note_launch(s);
     return e;
 }

@@ -57,8 +57,8 @@ cudaError_t launch_decode_paged_rows(tri_dtype dt, int G, const DecodePagedArgs&
                                      cudaStream_t s);
 
 // decode_paged_tc.cu: bf16 pages of a multiple of 8 rows, through the tensor
-// cores.  kmap, vmap: the pools as rows of 128, boxes of 64 dims x box_rows
-// rows with a 128-byte swizzle.
+// cores.  kmap, vmap: the pools as {64 dims, 8 rows, 2 halves, groups of 8
+// rows}, boxes of box_rows rows (box_rows / 8 groups), 128-byte swizzle.
 constexpr int kTcTile = 128;  // keys of one tile
 int decode_paged_box_rows(int64_t page_rows);  // 0: not served
 cudaError_t launch_decode_paged_tc(int G, const CUtensorMap& kmap, const CUtensorMap& vmap,
