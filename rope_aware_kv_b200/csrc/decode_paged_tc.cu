@@ -511,17 +511,22 @@ decode_paged_tc_kernel(const __grid_constant__ CUtensorMap kmap,
             named_sync(1, kTcMath);
             const bool whole = cur.tile0 >= p.begin && cur.t1 == cur.tile0 + cur.n_tiles;
             const uint32_t slot = part_slot(p, blockIdx.x, cur.tile0);
+            // Lane h finishes head h's sum, maximum and reciprocal.
+            const int hl = lane & 7;
+            const float den = (sm.wsum[0][hl] + sm.wsum[1][hl]) + (sm.wsum[2][hl] + sm.wsum[3][hl]);
+            const float inv = !whole ? 1.f : den == 0.f ? 0.f : 1.f / den;
+            float ml = 0.f;
 #pragma unroll
-            for (int h = 0; h < G; ++h) {
-                const float den = (sm.wsum[0][h] + sm.wsum[1][h]) + (sm.wsum[2][h] + sm.wsum[3][h]);
-                if (whole) {
-                    const int64_t row = static_cast<int64_t>(cur.i) * G + h;
-                    a.out[row * kD + tid] = den == 0.f ? 0.f : acc[h] / den;
-                    if (a.lse && tid == 0) a.lse[row] = lse_of(m[h], den);
-                } else {
-                    a.part[(slot * G + h) * kD + tid] = acc[h];
-                    if (tid == 0) a.part_ml[slot * G + h] = make_float2(m[h], den);
-                }
+            for (int h = 0; h < G; ++h) ml = hl == h ? m[h] : ml;
+            float* to = whole ? a.out + static_cast<int64_t>(cur.i) * G * kD
+                              : a.part + static_cast<int64_t>(slot) * G * kD;
+#pragma unroll
+            for (int h = 0; h < G; ++h) to[h * kD + tid] = acc[h] * __shfl_sync(0xffffffffu, inv, h);
+            if (tid < G) {
+                if (!whole)
+                    a.part_ml[slot * G + tid] = make_float2(ml, den);
+                else if (a.lse)
+                    a.lse[static_cast<int64_t>(cur.i) * G + tid] = lse_of(ml, den);
             }
             if (!whole) {
                 split1 = split_unit(p, cur.i, cur.tile0, cur.n_tiles);
