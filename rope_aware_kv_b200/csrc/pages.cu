@@ -33,6 +33,14 @@ __device__ __forceinline__ int64_t rows_added(const int32_t* n_add, int64_t seq,
     return x;
 }
 
+// Warps that move rows with bulk copies, and the shared memory of each.
+constexpr int kEngines = 8;
+constexpr int kWindow = 8192;
+struct CopyShared {
+    unsigned char window[kEngines][kWindow];
+    uint64_t landed[kEngines];
+};
+
 // ---------------------------------------------------------------------------
 // append
 // ---------------------------------------------------------------------------
@@ -88,46 +96,39 @@ __device__ void append_account(const AppendPagedArgs& a, int64_t i, const Append
                   static_cast<long long>(best) + 1);
 }
 
-// A warp copies new rows [x0, x1) (at most 8) of unit i, whose new rows begin
-// at `first`: half a warp moves a bf16 row (a whole one a float32 row) as
-// 16-byte vectors, all rows of both arrays in flight before the first store.
+// New rows [x0, x0 + m) (at most 8) of unit i in a warp's registers: half a warp
+// holds a bf16 row (a whole one a float32 row) as 16-byte vectors, all rows of
+// both arrays in flight before the first store.
 constexpr int kAppendFew = 8;
 
 template <int kVec>
-__device__ void append_rows(const AppendPagedArgs& a, int64_t i, int64_t u, int64_t first,
-                            int64_t x0, int64_t x1, int lane) {
-    constexpr int kPer = 32 / kVec;  // rows of one array in one instruction
-    constexpr int kIter = kAppendFew / kPer;
-    const uint4* kn = static_cast<const uint4*>(a.k_new);
-    const uint4* vn = static_cast<const uint4*>(a.v_new);
-    const int64_t x = x0 + lane;
-    const int64_t row = x < x1 ? paged_row(a.pc, u, first + x) : -1;
-    if (a.pos && x < x1) a.pos[u * a.cap + first + x] = a.pos_new[i * a.n_new + x];
-    const int64_t src0 = (i * a.n_new + x0) * kVec;
-    const int m = static_cast<int>(x1 - x0) * kVec;
-    uint4 kv[kIter], vv[kIter];
+struct NewRows {
+    static constexpr int kPer = 32 / kVec;  // rows of one array in one instruction
+    static constexpr int kIter = kAppendFew / kPer;
+    uint4 k[kIter], v[kIter];
+
+    __device__ __forceinline__ void read(const AppendPagedArgs& a, int64_t i, int64_t x0, int m, int lane) {
+        const int64_t src = (i * a.n_new + x0) * kVec + lane;
 #pragma unroll
-    for (int r = 0; r < kIter; ++r) {
-        const int e = r * 32 + lane;
-        if (e < m) kv[r] = ld_stream(kn + src0 + e);
+        for (int r = 0; r < kIter; ++r)
+            if (r * 32 + lane < m * kVec) k[r] = ld_stream(static_cast<const uint4*>(a.k_new) + src + r * 32);
+        if (!a.v) return;
+#pragma unroll
+        for (int r = 0; r < kIter; ++r)
+            if (r * 32 + lane < m * kVec) v[r] = ld_stream(static_cast<const uint4*>(a.v_new) + src + r * 32);
     }
-    if (a.v) {
+    // Into rows row0, row0 + 1, ... of unit u.
+    __device__ __forceinline__ void write(const AppendPagedArgs& a, int64_t u, int64_t row0, int m, int lane) {
+        const int64_t row = lane < m ? paged_row(a.pc, u, row0 + lane) : -1;
 #pragma unroll
         for (int r = 0; r < kIter; ++r) {
-            const int e = r * 32 + lane;
-            if (e < m) vv[r] = ld_stream(vn + src0 + e);
+            const int64_t dst = __shfl_sync(0xffffffffu, row, r * kPer + lane / kVec);
+            if (r * 32 + lane >= m * kVec || dst < 0) continue;
+            static_cast<uint4*>(a.k)[dst * kVec + lane % kVec] = k[r];
+            if (a.v) static_cast<uint4*>(a.v)[dst * kVec + lane % kVec] = v[r];
         }
     }
-#pragma unroll
-    for (int r = 0; r < kIter; ++r) {
-        const int64_t dst = __shfl_sync(0xffffffffu, row, r * kPer + lane / kVec);
-        const int e = r * 32 + lane;
-        if (e < m && dst >= 0) {
-            static_cast<uint4*>(a.k)[dst * kVec + lane % kVec] = kv[r];
-            if (a.v) static_cast<uint4*>(a.v)[dst * kVec + lane % kVec] = vv[r];
-        }
-    }
-}
+};
 
 // Few new rows a unit: one warp does all of a unit.
 
@@ -138,15 +139,20 @@ __global__ void __launch_bounds__(kThreads) append_few_kernel(const AppendPagedA
     if (i >= a.sl.n) return;
     const AppendUnit r = append_check(a, i, lane);
     if (r.first < 0) return;
-    append_rows<kVec>(a, i, r.unit, r.first, 0, r.add, lane);
+    const int m = static_cast<int>(r.add);
+    NewRows<kVec> rows;
+    rows.read(a, i, 0, m, lane);
+    rows.write(a, r.unit, r.first, m, lane);
+    if (a.pos && lane < m) a.pos[r.unit * a.cap + r.first + lane] = a.pos_new[i * a.n_new + lane];
     append_account(a, i, r, lane);
 }
 
 // Many: the units are looked over first (a CTA each, since a unit's positions
-// and pages are many), then every CTA copies kAppendChunk rows of one unit.
-constexpr int kAppendChunk = 64;
-
+// and pages are many), then every warp copies 8 rows of one unit, which it reads
+// while the look is under way.  (Bulk copies, 8 KB a window, took 130 us where
+// this takes 90: a ragged batch has many short windows.)
 __global__ void __launch_bounds__(kThreads) append_look_kernel(const AppendPagedArgs a) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int tid = threadIdx.x;
     const int64_t i = blockIdx.x;
     const int64_t u = slice_unit(a.sl, i);
@@ -175,7 +181,12 @@ __global__ void __launch_bounds__(kThreads) append_look_kernel(const AppendPaged
         a.first[i] = any ? -1 : static_cast<int32_t>(n);
         if (!any) a.n_valid[u] = static_cast<int32_t>(n + add);
     }
-    if (any || add == 0 || !a.p_cur) return;
+    if (any || add == 0) return;
+    if (a.pos) {
+#pragma unroll 8
+        for (int64_t x = tid; x < add; x += kThreads) a.pos[u * a.cap + n + x] = a.pos_new[i * a.n_new + x];
+    }
+    if (!a.p_cur) return;
     best = __reduce_max_sync(0xffffffffu, best);
     if ((tid & 31) == 0 && best != INT32_MIN)
         atomicMax(reinterpret_cast<long long*>(a.p_cur) + seq, static_cast<long long>(best) + 1);
@@ -185,14 +196,16 @@ template <int kVec>
 __global__ void __launch_bounds__(kThreads) append_copy_kernel(const AppendPagedArgs a, int chunks) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t i = blockIdx.x / chunks;
-    const int64_t first = a.first[i];
-    if (first < 0) return;
     const int64_t u = slice_unit(a.sl, i);
     const int64_t add = rows_added(a.n_add, u / (a.pc.n_units / a.pc.n_seq), a.n_new, nullptr);
-    constexpr int kRows = kAppendChunk / kWarps;
-    static_assert(kRows <= kAppendFew, "rows of a warp");
-    const int64_t x0 = static_cast<int64_t>(blockIdx.x % chunks) * kAppendChunk + warp * kRows;
-    if (x0 < add) append_rows<kVec>(a, i, u, first, x0, min(x0 + kRows, add), lane);
+    const int64_t x0 = (static_cast<int64_t>(blockIdx.x % chunks) * kWarps + warp) * kAppendFew;
+    if (x0 >= add) return;
+    const int m = static_cast<int>(min(add - x0, static_cast<int64_t>(kAppendFew)));
+    NewRows<kVec> rows;
+    rows.read(a, i, x0, m, lane);
+    wait_for_clear();  // (here: for the look kernel)
+    const int64_t first = __ldcg(a.first + i);
+    if (first >= 0) rows.write(a, u, first + x0, m, lane);
 }
 
 template <int kVec>
@@ -204,11 +217,11 @@ static cudaError_t launch_append_t(const AppendPagedArgs& a, cudaStream_t s) {
     }
     append_look_kernel<<<static_cast<unsigned>(a.sl.n), kThreads, 0, s>>>(a);
     note_launch(s);
-    const int64_t chunks = (a.n_new + kAppendChunk - 1) / kAppendChunk;
-    append_copy_kernel<kVec><<<static_cast<unsigned>(a.sl.n * chunks), kThreads, 0, s>>>(
-        a, static_cast<int>(chunks));
-    note_launch(s);
-    return cudaGetLastError();
+    const int64_t chunks = (a.n_new + kWarps * kAppendFew - 1) / (kWarps * kAppendFew);
+    const cudaError_t e = launch_early(append_copy_kernel<kVec>, static_cast<unsigned>(a.sl.n * chunks), kThreads, 0,
+                                       s, a, static_cast<int>(chunks));
+    if (e == cudaSuccess) note_launch(s);
+    return e;
 }
 
 cudaError_t launch_append_paged(tri_dtype dt, const AppendPagedArgs& a, cudaStream_t s) {
@@ -319,19 +332,13 @@ __device__ __forceinline__ PageSums sum_counts(const uint4* counts, uint32_t at)
 }
 
 // Copies of whole or part pages, of K and then of V, as one flat run of bytes
-// (`page_bytes` a page) cut into windows.  Every warp moves a window at a time
-// through its own 12 KB of shared memory with bulk copies, lane x the part of
-// the window that lies in its x-th page, so pages of any size keep 192 KB an SM
-// in flight.  page(c) gives copy c's source and destination page and its bytes.
-// A compaction that moves 698 MB takes 135 us (5.8 TB/s for the rows); 138 us
-// with 32 windows of 6 KB, 144 us with 64 of 3 KB, and 161 us with loads and
-// stores through registers (64 KB an SM in flight).
-constexpr int kWindow = 12288;
-struct CopyShared {
-    unsigned char window[kGridWarps][kWindow];
-    uint64_t landed[kGridWarps];
-};
-
+// (`page_bytes` a page) cut into windows.  kEngines warps a CTA move a window at
+// a time each, through their own shared memory with bulk copies, lane x the
+// part of the window that lies in its x-th page, so pages of any size keep 64 KB
+// an SM in flight.  page(c) gives copy c's source and destination page and its
+// bytes.  A compaction that moves 698 MB takes 126 us (6.2 TB/s for the rows);
+// more in flight is slower (133 us with 192 KB), and so are loads and stores
+// through registers (161 us with 64 KB).
 struct PageCopy {
     int32_t from, to;
     int64_t bytes;
@@ -343,6 +350,7 @@ __device__ __forceinline__ void copy_pages(void* k, void* v, int64_t copies, int
     extern __shared__ __align__(16) unsigned char smem[];
     CopyShared& sm = *reinterpret_cast<CopyShared*>(smem);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (warp >= kEngines) return;
     unsigned char* window = sm.window[warp];
     uint64_t* landed = &sm.landed[warp];
     if (lane == 0) {
@@ -355,7 +363,7 @@ __device__ __forceinline__ void copy_pages(void* k, void* v, int64_t copies, int
     const int64_t window_bytes = min(static_cast<int64_t>(kWindow), 31 * page_bytes);  // 32 pages at most
     const int64_t windows = (all + window_bytes - 1) / window_bytes;
     for (int64_t w = static_cast<int64_t>(warp) * gridDim.x + blockIdx.x; w < windows * (v ? 2 : 1);
-         w += static_cast<int64_t>(gridDim.x) * kGridWarps) {
+         w += static_cast<int64_t>(gridDim.x) * kEngines) {
         const bool second = w >= windows;
         char* pool = static_cast<char*>(second ? v : k);
         const int64_t b0 = (second ? w - windows : w) * window_bytes, b1 = min(b0 + window_bytes, all);
@@ -376,7 +384,8 @@ __device__ __forceinline__ void copy_pages(void* k, void* v, int64_t copies, int
         if (lane == 0) mbar_arrive_expect_tx(landed, bytes);
         __syncwarp();
         if (n > 0)
-            bulk_load(window + (at - b0), pool + p.from * page_bytes + off, static_cast<uint32_t>(n), landed);
+            bulk_load_hint(window + (at - b0), pool + p.from * page_bytes + off, static_cast<uint32_t>(n), landed,
+                           policy_evict_first());
         const bool ok = mbar_wait(landed, phase, flag);
         phase ^= 1;
         if (!__all_sync(0xffffffffu, ok)) break;
