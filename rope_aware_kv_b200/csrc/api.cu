@@ -570,7 +570,7 @@ tri_status make_group_map(CUtensorMap* map, const void* pool, int64_t rows, int 
 }
 
 struct DecodePagedWs {
-    size_t counters, part, part_ml, total;
+    size_t counters, part, part_ml, pieces, total;
 };
 DecodePagedWs decode_paged_ws(int64_t n_units, int G) {
     DecodePagedWs w;
@@ -579,6 +579,7 @@ DecodePagedWs decode_paged_ws(int64_t n_units, int G) {
     const size_t slots = 2 * decode_paged_ctas(static_cast<int>(sm_count_or_default()));
     w.part = c.take(slots * G * kD * 4);
     w.part_ml = c.take(slots * G * 8);
+    w.pieces = c.take(slots / 2 * decode_paged_piece_bytes(G));
     w.total = c.off;
     return w;
 }
@@ -1272,6 +1273,7 @@ tri_status tri_decode_attention_paged(const void* q, const void* k_pool, const v
     a.counters = reinterpret_cast<uint32_t*>(ws_at(ws, w.counters));
     a.part = reinterpret_cast<float*>(ws_at(ws, w.part));
     a.part_ml = reinterpret_cast<float2*>(ws_at(ws, w.part_ml));
+    a.pieces = reinterpret_cast<float*>(ws_at(ws, w.pieces));
     a.flag = ws_flag(ws);
     const int n_sm = static_cast<int>(sm_count_or_default());
     // Whole 8-row swizzle atoms of a page can be loaded as tensor tiles.

@@ -6,9 +6,11 @@
 // row j of the unit found through its page table (jaedaily.cn tutorial,
 // KV-compression objective: the softmax renormalised over the kept rows).
 //
-// rows kernel (any page size, both types).  Warps are independent: a warp
-// takes 32 keys at a time in groups of 8, copied row by row into its own
-// shared-memory ring (cp.async; a row without a page copies zeros).
+// rows kernel (any page size, both types).  A CTA's tiles of 32 keys are cut
+// into one contiguous run a warp; a warp streams its run, over changes of unit,
+// through its own shared-memory ring in groups of 8 keys, copied row by row
+// (cp.async; a row without a page copies zeros).  Units that lie in a warp's run
+// are finished by it; the others' pieces are joined at the CTA's end.
 //   scores   8 lanes share a key, 16 of its dims each, interleaved by 16-byte
 //            chunks so that the lanes' reads fall on different banks; a lane
 //            has two keys of the group at a time, which halves the reads of
@@ -33,7 +35,7 @@ __global__ void __launch_bounds__(256) decode_clear_kernel(uint32_t* flag, uint3
     if (i < n) counters[i] = 0;
 }
 
-constexpr int kRowThreads = 384;
+constexpr int kRowThreads = 320;
 constexpr int kRowWarps = kRowThreads / 32;
 constexpr int kRowTile = 32;    // keys a warp takes at a time
 constexpr int kGroup = 8;       // keys whose scores are formed together
@@ -41,16 +43,21 @@ constexpr int kRingBytes = 16384;  // of a warp: 2 groups of float32 rows, 4 of 
 
 constexpr int row_heads_pad(int G) { return G <= 2 ? 2 : G <= 4 ? 4 : 8; }
 
-// The results of the warps of one unit, which take the ring's place.
+// A warp's piece of a unit: (maximum, sum) and accumulator of every head.
 template <int G>
-constexpr size_t row_red_bytes() {
-    return static_cast<size_t>(kRowWarps) * G * (kD + 2) * sizeof(float);
+constexpr size_t row_piece_floats() {
+    return static_cast<size_t>(G) * (kD + 2);
 }
+struct RowPiece {
+    uint32_t i, tile0, n_tiles;
+    bool any;
+};
 
 struct RowShared {
-    float p[kRowWarps][kGroup * 8];  // weights [key][head]
-    float q[TRI_MAX_GROUP][kD];      // [head][piece][lane of 8][4 dims]
+    float p[kRowWarps][kGroup * 8];          // weights [key][head]
+    float q[kRowWarps][TRI_MAX_GROUP * kD];  // [head][piece][lane of 8][4 dims]
     unsigned char ring[kRowWarps][kRingBytes];
+    RowPiece piece[kRowWarps][2];            // of the unit that a warp's run begins in, and of its last one
 };
 
 __device__ __forceinline__ void copy16(void* dst, const void* src, bool valid) {
@@ -77,7 +84,7 @@ __device__ __forceinline__ void load4(const __nv_bfloat16* p, float2& a, float2&
 }
 
 template <typename T, int G>
-__global__ void __launch_bounds__(kRowThreads, 1) decode_paged_rows_kernel(const DecodePagedArgs a) {
+__global__ void __launch_bounds__(kRowThreads, 1) decode_paged_rows_kernel(const PageDivide divide, const DecodePagedArgs a) {
     constexpr int GP = row_heads_pad(G);     // heads of the butterfly
     constexpr int HP = (G + 1) / 2;          // pairs of heads
     constexpr int kRowBytes = kD * sizeof(T);
@@ -85,254 +92,323 @@ __global__ void __launch_bounds__(kRowThreads, 1) decode_paged_rows_kernel(const
     constexpr int kRing = kRingBytes / kGroupBytes;
     constexpr int kChunkDims = 16 / sizeof(T);           // dims of a 16-byte chunk
     constexpr int kGroups = kRowTile / kGroup;
+    constexpr size_t kPiece = row_piece_floats<G>();
     extern __shared__ __align__(16) unsigned char smem[];
     RowShared& sm = *reinterpret_cast<RowShared*>(smem);
-    float* red = reinterpret_cast<float*>(sm.ring);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int sub = lane & 7, quad = lane >> 3;  // lane of a key, key of four
-    const int64_t cap = a.pc.per_unit * a.pc.rows;
     const SplitPlan p = plan_split<kRowThreads>(a, kRowTile, kRowWarps);
-    SplitUnit split0 = {}, split1 = {};
-    int n_split = 0;
     unsigned char* ring = sm.ring[warp];
     float* pw = sm.p[warp];
+    float* qw = sm.q[warp];
+    // Pieces: the first one of a warp goes to global memory while the ring is
+    // in use, the last one takes the ring's place.
+    float* first_piece = a.pieces + (static_cast<int64_t>(blockIdx.x) * kRowWarps + warp) * kPiece;
+    float* last_piece = reinterpret_cast<float*>(ring);
     const char* kp = static_cast<const char*>(a.k);
     const char* vp = static_cast<const char*>(a.v);
 
-    uint32_t t = p.begin, i = p.unit, tile0 = p.tile0;
-    while (t < p.end) {
-        const int64_t u = slice_unit(a.sl, i);
-        const uint32_t n = clamp_nvalid(a.n_valid, u, cap, nullptr);
-        const uint32_t n_tiles = (n + kRowTile - 1) / kRowTile;
-        if (n_tiles == 0) {
-            ++i;
-            continue;
+    // ---- this warp's run of tiles [t0, t1) and its first unit ----
+    const uint32_t len = p.end - p.begin;
+    const uint32_t t0 = p.begin + len * warp / kRowWarps, t1 = p.begin + len * (warp + 1) / kRowWarps;
+    using Cursor = UnitCursor<kRowTile>;
+    Cursor cur = {};
+    if (t0 < t1) {
+        uint32_t i = p.unit, tile0 = p.tile0, rows = p.rows;
+        while (true) {  // 32 units at a time
+            const uint32_t n = Cursor::rows_of(a, i + lane);
+            const uint32_t nt = (n + kRowTile - 1) / kRowTile;
+            uint32_t incl = nt;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t x = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += x;
+            }
+            const uint32_t past = __ballot_sync(0xffffffffu, t0 < tile0 + incl);
+            if (past || i + 32 >= static_cast<uint32_t>(a.sl.n)) {
+                const int w = past ? __ffs(past) - 1 : 31;
+                i = min(i + w, static_cast<uint32_t>(a.sl.n) - 1);
+                tile0 += __shfl_sync(0xffffffffu, incl - nt, w);
+                rows = __shfl_sync(0xffffffffu, n, w);
+                break;
+            }
+            tile0 += __shfl_sync(0xffffffffu, incl, 31);
+            i += 32;
         }
-        const uint32_t b1 = min(n_tiles, p.end - tile0);  // tiles [b0, b1) of the unit
-        const uint32_t b0 = t - tile0;
-        // Q: piece r of lane s holds the 4 dims that it multiplies r-th.
-        for (int e = tid; e < G * (kD / 4); e += kRowThreads) {
-            const int h = e / (kD / 4), x = e % (kD / 4);  // dims 4 x ..
-            const int chunk = 4 * x / kChunkDims, part = x % (kChunkDims / 4);
+        cur.first(a, i, tile0, rows, t1);
+    }
+    if (lane < 2) sm.piece[warp][lane].any = false;
+
+    // Q of a unit: piece r of lane s holds the 4 dims that it multiplies r-th.
+    auto load_q = [&](uint32_t i) {
+        __syncwarp();
+#pragma unroll
+        for (int h = 0; h < G; ++h) {  // dims 4 lane ..
+            const int chunk = 4 * lane / kChunkDims, part = lane % (kChunkDims / 4);
             const int r = (chunk >> 3) * (kChunkDims / 4) + part;
             float2 lo, hi;
-            load4(static_cast<const T*>(a.q) + (static_cast<int64_t>(i) * G + h) * kD + 4 * x, lo, hi);
-            *reinterpret_cast<float4*>(&sm.q[h][(r * 8 + (chunk & 7)) * 4]) = make_float4(lo.x, lo.y, hi.x, hi.y);
+            load4(static_cast<const T*>(a.q) + (static_cast<int64_t>(i) * G + h) * kD + 4 * lane, lo, hi);
+            *reinterpret_cast<float4*>(&qw[h * kD + (r * 8 + (chunk & 7)) * 4]) = make_float4(lo.x, lo.y, hi.x, hi.y);
         }
-        float2 acc[4][HP];  // [dim][pair of heads]
+        __syncwarp();
+    };
+    float2 acc[4][HP];  // [dim][pair of heads]
+    // This lane's head; its l is over its own keys.
+    const int my_head = sub / (8 / GP);
+    float m = -INFINITY, l = 0.f;
+    auto begin_unit = [&](uint32_t i) {
+        load_q(i);
 #pragma unroll
         for (int x = 0; x < 4; ++x)
 #pragma unroll
             for (int h = 0; h < HP; ++h) acc[x][h] = make_float2(0.f, 0.f);
-        // This lane's head; its l is over its own keys.
-        const int my_head = sub / (8 / GP);
-        float m = -INFINITY, l = 0.f;
-        __syncthreads();
-
-        // Tiles b0 + warp, b0 + warp + kRowWarps, ...; their groups in one
-        // running order g = 0, 1, ... for the ring.
-        const uint32_t mt = b1 - b0 > warp ? (b1 - b0 - warp + kRowWarps - 1) / kRowWarps : 0;
-        const uint32_t n_groups = mt * kGroups;
-        // Physical row of this lane's key of a tile (-1: none).  Looked up a
-        // tile before its first copy is issued.
-        auto look_up = [&](uint32_t tile) -> int32_t {
-            const uint32_t j = (b0 + warp + tile * kRowWarps) * kRowTile + lane;
-            if (tile >= mt || j >= n) return -1;
-            const int64_t r = paged_row(a.pc, u, j);
-            if (r < 0) {
-                wait_for_clear();
-                raise_flag(a.flag, TRI_FLAG_INDEX_RANGE);
+        m = -INFINITY;
+        l = 0.f;
+    };
+    // The unit `w` ends in this run (or the run ends in it).
+    auto end_unit = [&](const Cursor& w) {
+        float sum = l;
+        sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+        const bool whole = w.tile0 >= t0 && w.tile0 + w.n_tiles <= t1;
+        const bool final = w.t1 == t1;
+        float* to = final ? last_piece : first_piece;
+        if (whole) {
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            float* o = a.out + static_cast<int64_t>(w.i) * G * kD + lane * 4;
+#pragma unroll
+            for (int h = 0; h < G; ++h) {
+                const float f = __shfl_sync(0xffffffffu, inv, h * (8 / GP));
+                const int x = h / 2;
+                *reinterpret_cast<float4*>(o + h * kD) =
+                    h & 1 ? make_float4(acc[0][x].y * f, acc[1][x].y * f, acc[2][x].y * f, acc[3][x].y * f)
+                          : make_float4(acc[0][x].x * f, acc[1][x].x * f, acc[2][x].x * f, acc[3][x].x * f);
             }
-            return static_cast<int32_t>(r);
-        };
-        int32_t row_ahead = look_up(0), row_issue = -1;
-        uint32_t have = 0, have_issue = 0;  // keys with a row, of the tile used and the one issued
-        auto issue = [&](uint32_t g) {
-            if (g < n_groups) {
-                const int gi = g % kGroups;
-                if (gi == 0) {
-                    row_issue = row_ahead;
-                    have_issue = __ballot_sync(0xffffffffu, row_issue >= 0);
-                    row_ahead = look_up(g / kGroups + 1);
-                }
-                unsigned char* slot = ring + (g % kRing) * kGroupBytes;
-                constexpr int kLanes = kRowBytes / 16;  // of one row
-#pragma unroll
-                for (int x = 0; x < kGroup; x += 32 / kLanes) {
-                    const int key = x + lane / kLanes, off = lane % kLanes * 16;
-                    const int32_t r = __shfl_sync(0xffffffffu, row_issue, gi * kGroup + key);
-                    const int64_t src = static_cast<int64_t>(r < 0 ? 0 : r) * kRowBytes + off;
-                    copy16(slot + key * kRowBytes + off, kp + src, r >= 0);
-                    copy16(slot + (kGroup + key) * kRowBytes + off, vp + src, r >= 0);
-                }
-            }
-            copy_commit();
-        };
-        for (int g = 0; g < kRing; ++g) issue(g);
-        // (The ring is at most one tile ahead, so the tile in use is the one
-        // issued or the one before it.)
-        uint32_t have_next = have_issue;
-        static_assert(kRing <= kGroups, "ring longer than a tile");
-        for (uint32_t g = 0; g < n_groups; ++g) {
-            const int gi = g % kGroups;
-            if (gi == 0) have = have_next;
-            copy_wait<kRing - 1>();
-            __syncwarp();
-            const unsigned char* slot = ring + (g % kRing) * kGroupBytes;
-            // ---- partial dot products of keys quad and quad + 4 ----
-            float2 s0[G], s1[G];
-#pragma unroll
-            for (int h = 0; h < G; ++h) s0[h] = s1[h] = make_float2(0.f, 0.f);
-            const T* k0 = reinterpret_cast<const T*>(slot + quad * kRowBytes);
-            const T* k1 = reinterpret_cast<const T*>(slot + (quad + 4) * kRowBytes);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int dim = (sub + 8 * (r / (kChunkDims / 4))) * kChunkDims + r % (kChunkDims / 4) * 4;
-                float2 x0, x1, y0, y1;
-                load4(k0 + dim, x0, x1);
-                load4(k1 + dim, y0, y1);
-#pragma unroll
-                for (int h = 0; h < G; ++h) {
-                    float2 q0, q1;
-                    load4(&sm.q[h][(r * 8 + sub) * 4], q0, q1);
-                    s0[h] = __ffma2_rn(x0, q0, s0[h]);
-                    s0[h] = __ffma2_rn(x1, q1, s0[h]);
-                    s1[h] = __ffma2_rn(y0, q0, s1[h]);
-                    s1[h] = __ffma2_rn(y1, q1, s1[h]);
-                }
-            }
-            // ---- the transposing butterfly over the key's 8 lanes ----
-            float sa[GP], sb[GP];
-#pragma unroll
-            for (int h = 0; h < GP; ++h) {
-                sa[h] = h < G ? s0[h < G ? h : 0].x + s0[h < G ? h : 0].y : 0.f;
-                sb[h] = h < G ? s1[h < G ? h : 0].x + s1[h < G ? h : 0].y : 0.f;
-            }
-            int o = 4;
-#pragma unroll
-            for (int count = GP; count > 1; count >>= 1) {
-                const bool up = sub & o;
-#pragma unroll
-                for (int x = 0; x < count / 2; ++x) {
-                    const float ka = up ? sa[x + count / 2] : sa[x], ga = up ? sa[x] : sa[x + count / 2];
-                    const float kb = up ? sb[x + count / 2] : sb[x], gb = up ? sb[x] : sb[x + count / 2];
-                    sa[x] = ka + __shfl_xor_sync(0xffffffffu, ga, o);
-                    sb[x] = kb + __shfl_xor_sync(0xffffffffu, gb, o);
-                }
-                o >>= 1;
-            }
-#pragma unroll
-            for (; o > 0; o >>= 1) {
-                sa[0] += __shfl_xor_sync(0xffffffffu, sa[0], o);
-                sb[0] += __shfl_xor_sync(0xffffffffu, sb[0], o);
-            }
-            // ---- online softmax of my_head ----
-            const uint32_t bits = have >> (gi * kGroup + quad);
-            const bool va = bits & 1, vb = bits & 16;
-            float mx = fmaxf(va ? sa[0] * a.scale_log2 : -INFINITY, vb ? sb[0] * a.scale_log2 : -INFINITY);
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-            const float m_new = fmaxf(m, mx);
-            const float base = m_new == -INFINITY ? 0.f : m_new;
-            // (one rounding of the small difference, not of the large product)
-            const float wa = va ? exp2f(fmaf(sa[0], a.scale_log2, -base)) : 0.f;
-            const float wb = vb ? exp2f(fmaf(sb[0], a.scale_log2, -base)) : 0.f;
-            if (__any_sync(0xffffffffu, m_new != m)) {
-                const float al = exp2f(m - base);
-                l *= al;
-#pragma unroll
-                for (int h = 0; h < HP; ++h) {
-                    const float a0 = __shfl_sync(0xffffffffu, al, 2 * h * (8 / GP));
-                    const float a1 = __shfl_sync(0xffffffffu, al, (2 * h + 1) * (8 / GP));
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        acc[x][h].x *= a0;
-                        acc[x][h].y *= a1;
-                    }
-                }
-                m = m_new;
-            }
-            l += wa + wb;
-            if (sub % (8 / GP) == 0) {
-                pw[quad * GP + my_head] = wa;
-                pw[(quad + 4) * GP + my_head] = wb;
-            }
-            __syncwarp();
-            // ---- values ----
-#pragma unroll
-            for (int key = 0; key < kGroup; ++key) {
-                float2 v01, v23;
-                load4(reinterpret_cast<const T*>(slot + (kGroup + key) * kRowBytes) + lane * 4, v01, v23);
-                float2 w[GP / 2];
-#pragma unroll
-                for (int h = 0; h < GP / 2; h += 2) {
-                    if constexpr (GP >= 4)
-                        load4(pw + key * GP + 2 * h, w[h], w[h + 1 < GP / 2 ? h + 1 : h]);
-                    else
-                        w[h] = *reinterpret_cast<const float2*>(pw + key * GP);
-                }
-#pragma unroll
-                for (int h = 0; h < HP; ++h) {
-                    acc[0][h] = __ffma2_rn(w[h], make_float2(v01.x, v01.x), acc[0][h]);
-                    acc[1][h] = __ffma2_rn(w[h], make_float2(v01.y, v01.y), acc[1][h]);
-                    acc[2][h] = __ffma2_rn(w[h], make_float2(v23.x, v23.x), acc[2][h]);
-                    acc[3][h] = __ffma2_rn(w[h], make_float2(v23.y, v23.y), acc[3][h]);
-                }
-            }
-            __syncwarp();  // the group's slot and the weights are rewritten
-            issue(g + kRing);
-            if ((g + kRing) % kGroups == 0) have_next = have_issue;
+            if (a.lse && quad == 0 && sub % (8 / GP) == 0 && my_head < G)
+                a.lse[static_cast<int64_t>(w.i) * G + my_head] = lse_of(m, sum);
+            return;
         }
-        copy_wait<0>();
-        // ---- the warps' results, joined in warp order ----
-        // l of my_head: over the keys' lanes.
-        l += __shfl_xor_sync(0xffffffffu, l, 8);
-        l += __shfl_xor_sync(0xffffffffu, l, 16);
-        __syncthreads();  // the rings are read; red takes their place
-        float* rw = red + warp * G * (kD + 2);
+        __syncwarp();  // (the ring's last reads)
 #pragma unroll
         for (int h = 0; h < G; ++h) {
-            float2* d = reinterpret_cast<float2*>(rw + h * (kD + 2) + 2 + lane * 4);
+            float2* d = reinterpret_cast<float2*>(to + h * (kD + 2) + 2 + lane * 4);
             const int x = h / 2;
             d[0] = h & 1 ? make_float2(acc[0][x].y, acc[1][x].y) : make_float2(acc[0][x].x, acc[1][x].x);
             d[1] = h & 1 ? make_float2(acc[2][x].y, acc[3][x].y) : make_float2(acc[2][x].x, acc[3][x].x);
         }
-        if (quad == 0 && sub % (8 / GP) == 0 && my_head < G) {
-            rw[my_head * (kD + 2)] = m;
-            rw[my_head * (kD + 2) + 1] = l;
+        if (quad == 0 && sub % (8 / GP) == 0 && my_head < G)
+            *reinterpret_cast<float2*>(to + my_head * (kD + 2)) = make_float2(m, sum);
+        if (lane == 0) sm.piece[warp][final ? 1 : 0] = RowPiece{w.i, w.tile0, w.n_tiles, true};
+    };
+
+    // ---- the stream: groups g = 0, 1, ... of tiles t0, t0 + 1, ... ----
+    const uint32_t n_groups = (t1 - t0) * kGroups;
+    // Physical row of this lane's key of tile t of unit w, from its page
+    // entry `page` (read a tile ahead of the first copy); -1: none.
+    Cursor ahead = cur;  // the unit of the tile to be issued next
+    auto key_of = [&](const Cursor& w, uint32_t t) { return (t - w.tile0) * kRowTile + lane; };
+    int32_t page_ahead = t0 < t1 ? ahead.page(divide, key_of(ahead, t0)) : -1;
+    int32_t row_issue = -1;
+    uint32_t have = 0, have_issue = 0;  // keys with a row, of the tile used and the one issued
+    auto issue = [&](uint32_t g) {
+        if (g < n_groups) {
+            const int gi = g % kGroups;
+            if (gi == 0) {
+                const uint32_t t = t0 + g / kGroups, j = key_of(ahead, t);
+                const bool ok = page_ahead >= 0 && page_ahead < a.pc.n_pages;
+                row_issue = ok ? page_ahead * divide.rows + (j - divide.slot(j) * divide.rows) : -1;
+                if (!ok && j < ahead.n) {
+                    wait_for_clear();
+                    raise_flag(a.flag, TRI_FLAG_INDEX_RANGE);
+                }
+                have_issue = __ballot_sync(0xffffffffu, ok);
+                if (t + 1 < t1) {
+                    if (t + 1 == ahead.t1) ahead = ahead.next(a, t1);
+                    page_ahead = ahead.page(divide, key_of(ahead, t + 1));
+                }
+            }
+            unsigned char* slot = ring + (g % kRing) * kGroupBytes;
+            constexpr int kLanes = kRowBytes / 16;  // of one row
+#pragma unroll
+            for (int x = 0; x < kGroup; x += 32 / kLanes) {
+                const int key = x + lane / kLanes, off = lane % kLanes * 16;
+                const int32_t r = __shfl_sync(0xffffffffu, row_issue, gi * kGroup + key);
+                const int64_t src = static_cast<int64_t>(r < 0 ? 0 : r) * kRowBytes + off;
+                copy16(slot + key * kRowBytes + off, kp + src, r >= 0);
+                copy16(slot + (kGroup + key) * kRowBytes + off, vp + src, r >= 0);
+            }
         }
-        __syncthreads();
-        const bool whole = b0 == 0 && b1 == n_tiles;
-        const uint32_t slot = part_slot(p, blockIdx.x, tile0);
+        copy_commit();
+    };
+    for (int g = 0; g < kRing; ++g) issue(g);
+    // (The ring is at most one tile ahead, so the tile in use is the one
+    // issued or the one before it.)
+    uint32_t have_next = have_issue;
+    static_assert(kRing <= kGroups, "ring longer than a tile");
+    if (n_groups) begin_unit(cur.i);
+    for (uint32_t g = 0; g < n_groups; ++g) {
+        const int gi = g % kGroups;
+        if (gi == 0) {
+            have = have_next;
+            if (t0 + g / kGroups == cur.t1) {
+                end_unit(cur);
+                cur = cur.next(a, t1);
+                begin_unit(cur.i);
+            }
+        }
+        copy_wait<kRing - 1>();
+        __syncwarp();
+        const unsigned char* slot = ring + (g % kRing) * kGroupBytes;
+        // ---- partial dot products of keys quad and quad + 4 ----
+        float2 s0[G], s1[G];
+#pragma unroll
+        for (int h = 0; h < G; ++h) s0[h] = s1[h] = make_float2(0.f, 0.f);
+        const T* k0 = reinterpret_cast<const T*>(slot + quad * kRowBytes);
+        const T* k1 = reinterpret_cast<const T*>(slot + (quad + 4) * kRowBytes);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int dim = (sub + 8 * (r / (kChunkDims / 4))) * kChunkDims + r % (kChunkDims / 4) * 4;
+            float2 x0, x1, y0, y1;
+            load4(k0 + dim, x0, x1);
+            load4(k1 + dim, y0, y1);
+#pragma unroll
+            for (int h = 0; h < G; ++h) {
+                float2 q0, q1;
+                load4(&qw[h * kD + (r * 8 + sub) * 4], q0, q1);
+                s0[h] = __ffma2_rn(x0, q0, s0[h]);
+                s0[h] = __ffma2_rn(x1, q1, s0[h]);
+                s1[h] = __ffma2_rn(y0, q0, s1[h]);
+                s1[h] = __ffma2_rn(y1, q1, s1[h]);
+            }
+        }
+        // ---- the transposing butterfly over the key's 8 lanes ----
+        float sa[GP], sb[GP];
+#pragma unroll
+        for (int h = 0; h < GP; ++h) {
+            sa[h] = h < G ? s0[h < G ? h : 0].x + s0[h < G ? h : 0].y : 0.f;
+            sb[h] = h < G ? s1[h < G ? h : 0].x + s1[h < G ? h : 0].y : 0.f;
+        }
+        int o = 4;
+#pragma unroll
+        for (int count = GP; count > 1; count >>= 1) {
+            const bool up = sub & o;
+#pragma unroll
+            for (int x = 0; x < count / 2; ++x) {
+                const float ka = up ? sa[x + count / 2] : sa[x], ga = up ? sa[x] : sa[x + count / 2];
+                const float kb = up ? sb[x + count / 2] : sb[x], gb = up ? sb[x] : sb[x + count / 2];
+                sa[x] = ka + __shfl_xor_sync(0xffffffffu, ga, o);
+                sb[x] = kb + __shfl_xor_sync(0xffffffffu, gb, o);
+            }
+            o >>= 1;
+        }
+#pragma unroll
+        for (; o > 0; o >>= 1) {
+            sa[0] += __shfl_xor_sync(0xffffffffu, sa[0], o);
+            sb[0] += __shfl_xor_sync(0xffffffffu, sb[0], o);
+        }
+        // ---- online softmax of my_head ----
+        const uint32_t bits = have >> (gi * kGroup + quad);
+        const bool va = bits & 1, vb = bits & 16;
+        float mx = fmaxf(va ? sa[0] * a.scale_log2 : -INFINITY, vb ? sb[0] * a.scale_log2 : -INFINITY);
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+        const float m_new = fmaxf(m, mx);
+        const float base = m_new == -INFINITY ? 0.f : m_new;
+        // (one rounding of the small difference, not of the large product)
+        const float wa = va ? exp2f(fmaf(sa[0], a.scale_log2, -base)) : 0.f;
+        const float wb = vb ? exp2f(fmaf(sb[0], a.scale_log2, -base)) : 0.f;
+        if (__any_sync(0xffffffffu, m_new != m)) {
+            const float al = exp2f(m - base);
+            l *= al;
+#pragma unroll
+            for (int h = 0; h < HP; ++h) {
+                const float a0 = __shfl_sync(0xffffffffu, al, 2 * h * (8 / GP));
+                const float a1 = __shfl_sync(0xffffffffu, al, (2 * h + 1) * (8 / GP));
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    acc[x][h].x *= a0;
+                    acc[x][h].y *= a1;
+                }
+            }
+            m = m_new;
+        }
+        l += wa + wb;
+        if (sub % (8 / GP) == 0) {
+            pw[quad * GP + my_head] = wa;
+            pw[(quad + 4) * GP + my_head] = wb;
+        }
+        __syncwarp();
+        // ---- values ----
+#pragma unroll
+        for (int key = 0; key < kGroup; ++key) {
+            float2 v01, v23;
+            load4(reinterpret_cast<const T*>(slot + (kGroup + key) * kRowBytes) + lane * 4, v01, v23);
+            float2 w[GP / 2];
+#pragma unroll
+            for (int h = 0; h < GP / 2; h += 2) {
+                if constexpr (GP >= 4)
+                    load4(pw + key * GP + 2 * h, w[h], w[h + 1 < GP / 2 ? h + 1 : h]);
+                else
+                    w[h] = *reinterpret_cast<const float2*>(pw + key * GP);
+            }
+#pragma unroll
+            for (int h = 0; h < HP; ++h) {
+                acc[0][h] = __ffma2_rn(w[h], make_float2(v01.x, v01.x), acc[0][h]);
+                acc[1][h] = __ffma2_rn(w[h], make_float2(v01.y, v01.y), acc[1][h]);
+                acc[2][h] = __ffma2_rn(w[h], make_float2(v23.x, v23.x), acc[2][h]);
+                acc[3][h] = __ffma2_rn(w[h], make_float2(v23.y, v23.y), acc[3][h]);
+            }
+        }
+        __syncwarp();  // the group's slot and the weights are rewritten
+        issue(g + kRing);
+        if ((g + kRing) % kGroups == 0) have_next = have_issue;
+    }
+    copy_wait<0>();
+    if (n_groups) end_unit(cur);
+    // ---- the pieces, in the order of the warps; those of one unit follow one another ----
+    __syncthreads();
+    SplitUnit split0 = {}, split1 = {};
+    int n_split = 0;
+#pragma unroll 1
+    for (int e0 = 0; e0 < 2 * kRowWarps;) {
+        if (!sm.piece[e0 >> 1][e0 & 1].any) {
+            ++e0;
+            continue;
+        }
+        const RowPiece w = sm.piece[e0 >> 1][e0 & 1];
+        int e1 = e0 + 1;
+        while (e1 < 2 * kRowWarps && (!sm.piece[e1 >> 1][e1 & 1].any || sm.piece[e1 >> 1][e1 & 1].i == w.i)) ++e1;
+        const bool whole = w.tile0 >= p.begin && w.tile0 + w.n_tiles <= p.end;
+        const uint32_t slot = part_slot(p, blockIdx.x, w.tile0);
         for (int e = tid; e < G * kD; e += kRowThreads) {
             const int h = e / kD, d = e % kD;
-            float M = -INFINITY;
-#pragma unroll
-            for (int w = 0; w < kRowWarps; ++w) M = fmaxf(M, red[(w * G + h) * (kD + 2)]);
-            float num = 0.f, den = 0.f;
-#pragma unroll
-            for (int w = 0; w < kRowWarps; ++w) {
-                const float* x = red + (w * G + h) * (kD + 2);
-                const float f = x[0] == -INFINITY ? 0.f : exp2f(x[0] - M);
-                num = fmaf(f, x[2 + d], num);
-                den = fmaf(f, x[1], den);
+            float M = -INFINITY, num = 0.f, den = 0.f;
+            for (int x = e0; x < e1; ++x) {
+                if (!sm.piece[x >> 1][x & 1].any) continue;
+                const float* f = (x & 1 ? reinterpret_cast<const float*>(sm.ring[x >> 1])
+                                        : a.pieces + (static_cast<int64_t>(blockIdx.x) * kRowWarps + (x >> 1)) * kPiece) +
+                                 h * (kD + 2);
+                const float m_new = fmaxf(M, f[0]);
+                const float base = m_new == -INFINITY ? 0.f : m_new;
+                const float fa = exp2f(M - base), fb = exp2f(f[0] - base);
+                num = fmaf(num, fa, fb * f[2 + d]);
+                den = fmaf(den, fa, fb * f[1]);
+                M = m_new;
             }
             if (whole) {
-                a.out[(static_cast<int64_t>(i) * G + h) * kD + d] = den == 0.f ? 0.f : num / den;
-                if (a.lse && d == 0) a.lse[static_cast<int64_t>(i) * G + h] = lse_of(M, den);
+                const int64_t row = static_cast<int64_t>(w.i) * G + h;
+                a.out[row * kD + d] = den == 0.f ? 0.f : num / den;
+                if (a.lse && d == 0) a.lse[row] = lse_of(M, den);
             } else {
                 a.part[(static_cast<int64_t>(slot) * G + h) * kD + d] = num;
                 if (d == 0) a.part_ml[slot * G + h] = make_float2(M, den);
             }
         }
         if (!whole) {
-            split1 = split_unit(p, i, tile0, n_tiles);
+            split1 = split_unit(p, w.i, w.tile0, w.n_tiles);
             if (n_split++ == 0) split0 = split1;
         }
-        __syncthreads();  // red and Q are rewritten by the next unit
-        t = tile0 + b1;
-        tile0 += n_tiles;
-        ++i;
+        e0 = e1;
     }
     join_split_units<kRowWarps, 0, 8>(a, G, n_split, split0, split1);
     write_empty_units(a, G);
@@ -342,6 +418,8 @@ __global__ void __launch_bounds__(kRowThreads, 1) decode_paged_rows_kernel(const
 // host side
 // ---------------------------------------------------------------------------
 int decode_paged_ctas(int n_sm) { return n_sm; }
+
+size_t decode_paged_piece_bytes(int G) { return static_cast<size_t>(kRowWarps) * G * (kD + 2) * sizeof(float); }
 
 cudaError_t launch_decode_paged_clear(const DecodePagedArgs& a, cudaStream_t s) {
     decode_clear_kernel<<<static_cast<unsigned>((a.sl.n + 255) / 256), 256, 0, s>>>(a.flag, a.counters,
@@ -353,14 +431,14 @@ cudaError_t launch_decode_paged_clear(const DecodePagedArgs& a, cudaStream_t s) 
 template <typename T, int G>
 static cudaError_t launch_rows(const DecodePagedArgs& a, int n_sm, cudaStream_t s) {
     constexpr size_t smem = sizeof(RowShared);
-    static_assert(row_red_bytes<G>() <= sizeof(RowShared::ring) && smem <= 227 * 1024, "shared memory");
+    static_assert(row_piece_floats<G>() * 4 <= kRingBytes && smem <= 227 * 1024, "shared memory");
     auto* fn = decode_paged_rows_kernel<T, G>;
     struct Key {};
     cudaError_t e = allow_smem<Key>(reinterpret_cast<const void*>(fn), smem);
     if (e != cudaSuccess) return e;
     e = launch_decode_paged_clear(a, s);
     if (e != cudaSuccess) return e;
-    e = launch_early(fn, decode_paged_ctas(n_sm), kRowThreads, smem, s, a);
+    e = launch_early(fn, decode_paged_ctas(n_sm), kRowThreads, smem, s, page_divide(a.pc.rows), a);
     if (e == cudaSuccess) note_launch(s);
     return e;
 }

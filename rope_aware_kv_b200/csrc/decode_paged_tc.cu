@@ -168,59 +168,7 @@ __device__ __forceinline__ float reduce8(float (&x)[8], Op op) {
     return op(x[0], __shfl_xor_sync(0xffffffffu, x[0], 1));
 }
 
-// j / page_rows for j < 2^31 by a multiplication: with 2^l >= d > 2^(l-1) and
-// m = floor(2^(31+l) / d) + 1, the product m d exceeds 2^(31+l) by at most 2^l,
-// so floor(j m / 2^(31+l)) is exact.  (d >= 8 here.)
-struct PageDivide {
-    uint32_t m, shift, rows;
-    __device__ __forceinline__ uint32_t slot(uint32_t j) const { return __umulhi(j, m) >> shift; }
-};
-
-// A unit of the CTA's range, and the row counts of the two units behind it
-// (read ahead).
-struct TcUnit {
-    uint32_t i, tile0, n, n_tiles;
-    uint32_t t1;           // its tiles in the range end here
-    uint32_t n1, n2;
-    const int32_t* pages;  // its page table row
-
-    __device__ static uint32_t rows_of(const DecodePagedArgs& a, uint32_t i) {
-        if (i >= static_cast<uint32_t>(a.sl.n)) return 0;
-        return clamp_nvalid(a.n_valid, slice_unit(a.sl, i), a.pc.per_unit * a.pc.rows, nullptr);
-    }
-    __device__ void set(const DecodePagedArgs& a, const SplitPlan& p, uint32_t rows) {
-        n = rows;
-        n_tiles = (n + kTcTile - 1) / kTcTile;
-        t1 = min(tile0 + n_tiles, p.end);
-        pages = a.pc.table + slice_unit(a.sl, i) * a.pc.per_unit;
-    }
-    __device__ void first(const DecodePagedArgs& a, const SplitPlan& p) {
-        i = p.unit;
-        tile0 = p.tile0;
-        set(a, p, p.rows);
-        n1 = rows_of(a, i + 1);
-        n2 = rows_of(a, i + 2);
-    }
-    // The next unit with rows (there is one while t1 < p.end).
-    __device__ TcUnit next(const DecodePagedArgs& a, const SplitPlan& p) const {
-        TcUnit x;
-        x.tile0 = tile0 + n_tiles;
-        x.i = i + 1;
-        x.n1 = n2;
-        uint32_t rows = n1;
-        while (rows == 0 && x.i + 1 < static_cast<uint32_t>(a.sl.n)) {
-            rows = x.n1;
-            ++x.i;
-            x.n1 = rows_of(a, x.i + 1);
-        }
-        x.i = min(x.i, static_cast<uint32_t>(a.sl.n) - 1);
-        x.set(a, p, rows);
-        x.n2 = rows_of(a, x.i + 2);
-        return x;
-    }
-    // Page entry of row j, -1 past the last row.
-    __device__ int32_t page(const PageDivide& d, uint32_t j) const { return j < n ? pages[d.slot(j)] : -1; }
-};
+using TcUnit = UnitCursor<kTcTile>;
 
 template <int G>
 __global__ void __launch_bounds__(kTcThreads, 1)
@@ -278,7 +226,7 @@ decode_paged_tc_kernel(const __grid_constant__ CUtensorMap kmap,
         };
         int32_t page = -1;
         if (n_it) {
-            cur.first(a, p);
+            cur.first(a, p.unit, p.tile0, p.rows, p.end);
             page = look_up(cur, p.begin);
         }
         uint32_t it = 0;
@@ -288,7 +236,7 @@ decode_paged_tc_kernel(const __grid_constant__ CUtensorMap kmap,
             const uint32_t parity = ((it / kTcStages) & 1) ^ 1;
             const uint32_t j = (t - cur.tile0) * kTcTile + lane * box_rows;
             const bool wanted = lane < n_boxes && j < cur.n;
-            if (t + 1 == cur.t1 && it + 1 < n_it) cur = cur.next(a, p);
+            if (t + 1 == cur.t1 && it + 1 < n_it) cur = cur.next(a, p.end);
             const int32_t page_next = it + 1 < n_it ? look_up(cur, t + 1) : -1;
             const bool load = page >= 0 && page < a.pc.n_pages;
             if (wanted && !load) {
@@ -407,7 +355,7 @@ decode_paged_tc_kernel(const __grid_constant__ CUtensorMap kmap,
         int32_t page = -1;  // entry of this thread's key (read a tile ahead)
         if (n_it) {
             read_q(p.unit);
-            cur.first(a, p);
+            cur.first(a, p.unit, p.tile0, p.rows, p.end);
             page = cur.page(divide, (p.begin - cur.tile0) * kTcTile + tid);
             store_q(0);
             if (tid == 0) sm.q_next = p.begin + 1 < cur.t1 ? 2 : 0;
@@ -421,7 +369,7 @@ decode_paged_tc_kernel(const __grid_constant__ CUtensorMap kmap,
             const bool valid = page >= 0 && page < a.pc.n_pages;
             TcUnit nxt = cur;
             if (ends && more) {
-                nxt = cur.next(a, p);
+                nxt = cur.next(a, p.end);
                 read_q(nxt.i);
             }
             page = more ? nxt.page(divide, (t + 1 - nxt.tile0) * kTcTile + tid) : -1;
@@ -566,13 +514,8 @@ static cudaError_t launch_tc(const CUtensorMap& kmap, const CUtensorMap& vmap, i
     if (e != cudaSuccess) return e;
     e = launch_decode_paged_clear(a, s);
     if (e != cudaSuccess) return e;
-    PageDivide d;
-    d.rows = static_cast<uint32_t>(a.pc.rows);
-    uint32_t l = 3;
-    while ((1ull << l) < d.rows) ++l;
-    d.m = static_cast<uint32_t>((1ull << (31 + l)) / d.rows + 1);
-    d.shift = l - 1;
-    e = launch_early(fn, decode_paged_ctas(n_sm), kTcThreads, smem, s, kmap, vmap, box_rows, d, a);
+    e = launch_early(fn, decode_paged_ctas(n_sm), kTcThreads, smem, s, kmap, vmap, box_rows,
+                     page_divide(a.pc.rows), a);
     if (e == cudaSuccess) note_launch(s);
     return e;
 }

@@ -46,9 +46,11 @@ struct DecodePagedArgs {
     // [2 * ctas][G][128] and (maximum, sum) [2 * ctas][G].
     float* part;
     float2* part_ml;
+    float* pieces;           // scratch of the row kernel, decode_paged_piece_bytes a CTA
     uint32_t* flag;
 };
 int decode_paged_ctas(int n_sm);
+size_t decode_paged_piece_bytes(int G);
 // The first kernel of the call: clears the flag word and the counters while
 // the second one begins.
 cudaError_t launch_decode_paged_clear(const DecodePagedArgs& a, cudaStream_t s);

@@ -121,6 +121,71 @@ __device__ SplitPlan plan_split(const DecodePagedArgs& a, int tile, uint32_t min
     return p;
 }
 
+// j / page_rows for j < 2^31 by a multiplication: with 2^l >= d > 2^(l-1) and
+// m = floor(2^(31+l) / d) + 1, the product m d exceeds 2^(31+l) by at most 2^l,
+// so floor(j m / 2^(31+l)) is exact.  (d = 1 has no such m: m = 0.)
+struct PageDivide {
+    uint32_t m, shift, rows;
+    __device__ __forceinline__ uint32_t slot(uint32_t j) const { return m ? __umulhi(j, m) >> shift : j; }
+};
+inline PageDivide page_divide(int64_t rows) {
+    PageDivide d = {0, 0, static_cast<uint32_t>(rows)};
+    if (rows == 1) return d;
+    uint32_t l = 1;
+    while ((1ull << l) < d.rows) ++l;
+    d.m = static_cast<uint32_t>((1ull << (31 + l)) / d.rows + 1);
+    d.shift = l - 1;
+    return d;
+}
+
+// A unit of a range of tiles that ends at `end`, and the row counts of the two
+// units behind it (read ahead).
+template <int kTile>
+struct UnitCursor {
+    uint32_t i, tile0, n, n_tiles;
+    uint32_t t1;           // its tiles in the range end here
+    uint32_t n1, n2;
+    const int32_t* pages;  // its page table row
+
+    __device__ static uint32_t rows_of(const DecodePagedArgs& a, uint32_t i) {
+        if (i >= static_cast<uint32_t>(a.sl.n)) return 0;
+        return clamp_nvalid(a.n_valid, slice_unit(a.sl, i), a.pc.per_unit * a.pc.rows, nullptr);
+    }
+    __device__ void set(const DecodePagedArgs& a, uint32_t end, uint32_t rows) {
+        n = rows;
+        n_tiles = (n + kTile - 1) / kTile;
+        t1 = min(tile0 + n_tiles, end);
+        pages = a.pc.table + slice_unit(a.sl, i) * a.pc.per_unit;
+    }
+    __device__ void first(const DecodePagedArgs& a, uint32_t unit, uint32_t unit_tile0, uint32_t rows,
+                          uint32_t end) {
+        i = unit;
+        tile0 = unit_tile0;
+        set(a, end, rows);
+        n1 = rows_of(a, i + 1);
+        n2 = rows_of(a, i + 2);
+    }
+    // The next unit with rows (there is one while t1 < end).
+    __device__ UnitCursor next(const DecodePagedArgs& a, uint32_t end) const {
+        UnitCursor x;
+        x.tile0 = tile0 + n_tiles;
+        x.i = i + 1;
+        x.n1 = n2;
+        uint32_t rows = n1;
+        while (rows == 0 && x.i + 1 < static_cast<uint32_t>(a.sl.n)) {
+            rows = x.n1;
+            ++x.i;
+            x.n1 = rows_of(a, x.i + 1);
+        }
+        x.i = min(x.i, static_cast<uint32_t>(a.sl.n) - 1);
+        x.set(a, end, rows);
+        x.n2 = rows_of(a, x.i + 2);
+        return x;
+    }
+    // Page entry of row j, -1 past the last row.
+    __device__ int32_t page(const PageDivide& d, uint32_t j) const { return j < n ? pages[d.slot(j)] : -1; }
+};
+
 // The first kernel of the call clears the flag word and the counters and lets
 // the second one start at once; that one waits here before it touches them.
 __device__ __forceinline__ void wait_for_clear() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
