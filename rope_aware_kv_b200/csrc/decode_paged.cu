@@ -43,11 +43,9 @@ constexpr int kRingBytes = 16384;  // of a warp: 2 groups of float32 rows, 4 of 
 
 constexpr int row_heads_pad(int G) { return G <= 2 ? 2 : G <= 4 ? 4 : 8; }
 
-// A warp's piece of a unit: (maximum, sum) and accumulator of every head.
-template <int G>
-constexpr size_t row_piece_floats() {
-    return static_cast<size_t>(G) * (kD + 2);
-}
+// A warp's piece of a unit: the accumulators of every head (maxima and sums
+// stay in shared memory).
+constexpr size_t row_piece_floats(int G) { return static_cast<size_t>(G) * kD; }
 struct RowPiece {
     uint32_t i, tile0, n_tiles;
     bool any;
@@ -57,7 +55,8 @@ struct RowShared {
     float p[kRowWarps][kGroup * 8];          // weights [key][head]
     float q[kRowWarps][TRI_MAX_GROUP * kD];  // [head][piece][lane of 8][4 dims]
     unsigned char ring[kRowWarps][kRingBytes];
-    RowPiece piece[kRowWarps][2];            // of the unit that a warp's run begins in, and of its last one
+    RowPiece piece[2 * kRowWarps];           // [warp][of the unit its run begins in, of its last unit]
+    float2 piece_ml[2 * kRowWarps][TRI_MAX_GROUP];
 };
 
 __device__ __forceinline__ void copy16(void* dst, const void* src, bool valid) {
@@ -83,6 +82,18 @@ __device__ __forceinline__ void load4(const __nv_bfloat16* p, float2& a, float2&
     b = make_float2(bf16_lo(x.y), bf16_hi(x.y));
 }
 
+// The same from global memory that nothing writes meanwhile.
+__device__ __forceinline__ void read4(const float* p, float2& a, float2& b) {
+    const float4 x = __ldg(reinterpret_cast<const float4*>(p));
+    a = make_float2(x.x, x.y);
+    b = make_float2(x.z, x.w);
+}
+__device__ __forceinline__ void read4(const __nv_bfloat16* p, float2& a, float2& b) {
+    const uint2 x = __ldg(reinterpret_cast<const uint2*>(p));
+    a = make_float2(bf16_lo(x.x), bf16_hi(x.x));
+    b = make_float2(bf16_lo(x.y), bf16_hi(x.y));
+}
+
 template <typename T, int G>
 __global__ void __launch_bounds__(kRowThreads, 1) decode_paged_rows_kernel(const PageDivide divide, const DecodePagedArgs a) {
     constexpr int GP = row_heads_pad(G);     // heads of the butterfly
@@ -92,7 +103,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) decode_paged_rows_kernel(const
     constexpr int kRing = kRingBytes / kGroupBytes;
     constexpr int kChunkDims = 16 / sizeof(T);           // dims of a 16-byte chunk
     constexpr int kGroups = kRowTile / kGroup;
-    constexpr size_t kPiece = row_piece_floats<G>();
+    constexpr size_t kPiece = row_piece_floats(G);
     extern __shared__ __align__(16) unsigned char smem[];
     RowShared& sm = *reinterpret_cast<RowShared*>(smem);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -115,7 +126,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) decode_paged_rows_kernel(const
     Cursor cur = {};
     if (t0 < t1) {
         uint32_t i = p.unit, tile0 = p.tile0, rows = p.rows;
-        while (true) {  // 32 units at a time
+        while (t0 >= tile0 + (rows + kRowTile - 1) / kRowTile) {  // 32 units at a time
             const uint32_t n = Cursor::rows_of(a, i + lane);
             const uint32_t nt = (n + kRowTile - 1) / kRowTile;
             uint32_t incl = nt;
@@ -137,19 +148,21 @@ __global__ void __launch_bounds__(kRowThreads, 1) decode_paged_rows_kernel(const
         }
         cur.first(a, i, tile0, rows, t1);
     }
-    if (lane < 2) sm.piece[warp][lane].any = false;
+    if (lane < 2) sm.piece[2 * warp + lane].any = false;
 
     // Q of a unit: piece r of lane s holds the 4 dims that it multiplies r-th.
     auto load_q = [&](uint32_t i) {
+        const T* q = static_cast<const T*>(a.q) + static_cast<int64_t>(i) * G * kD + 4 * lane;
+        float2 x[G][2];
+#pragma unroll
+        for (int h = 0; h < G; ++h) read4(q + h * kD, x[h][0], x[h][1]);
+        const int chunk = 4 * lane / kChunkDims, part = lane % (kChunkDims / 4);  // dims 4 lane ..
+        const int r = (chunk >> 3) * (kChunkDims / 4) + part;
         __syncwarp();
 #pragma unroll
-        for (int h = 0; h < G; ++h) {  // dims 4 lane ..
-            const int chunk = 4 * lane / kChunkDims, part = lane % (kChunkDims / 4);
-            const int r = (chunk >> 3) * (kChunkDims / 4) + part;
-            float2 lo, hi;
-            load4(static_cast<const T*>(a.q) + (static_cast<int64_t>(i) * G + h) * kD + 4 * lane, lo, hi);
-            *reinterpret_cast<float4*>(&qw[h * kD + (r * 8 + (chunk & 7)) * 4]) = make_float4(lo.x, lo.y, hi.x, hi.y);
-        }
+        for (int h = 0; h < G; ++h)
+            *reinterpret_cast<float4*>(&qw[h * kD + (r * 8 + (chunk & 7)) * 4]) =
+                make_float4(x[h][0].x, x[h][0].y, x[h][1].x, x[h][1].y);
         __syncwarp();
     };
     float2 acc[4][HP];  // [dim][pair of heads]
@@ -191,14 +204,14 @@ __global__ void __launch_bounds__(kRowThreads, 1) decode_paged_rows_kernel(const
         __syncwarp();  // (the ring's last reads)
 #pragma unroll
         for (int h = 0; h < G; ++h) {
-            float2* d = reinterpret_cast<float2*>(to + h * (kD + 2) + 2 + lane * 4);
             const int x = h / 2;
-            d[0] = h & 1 ? make_float2(acc[0][x].y, acc[1][x].y) : make_float2(acc[0][x].x, acc[1][x].x);
-            d[1] = h & 1 ? make_float2(acc[2][x].y, acc[3][x].y) : make_float2(acc[2][x].x, acc[3][x].x);
+            *reinterpret_cast<float4*>(to + h * kD + lane * 4) =
+                h & 1 ? make_float4(acc[0][x].y, acc[1][x].y, acc[2][x].y, acc[3][x].y)
+                      : make_float4(acc[0][x].x, acc[1][x].x, acc[2][x].x, acc[3][x].x);
         }
-        if (quad == 0 && sub % (8 / GP) == 0 && my_head < G)
-            *reinterpret_cast<float2*>(to + my_head * (kD + 2)) = make_float2(m, sum);
-        if (lane == 0) sm.piece[warp][final ? 1 : 0] = RowPiece{w.i, w.tile0, w.n_tiles, true};
+        const int e = 2 * warp + (final ? 1 : 0);
+        if (quad == 0 && sub % (8 / GP) == 0 && my_head < G) sm.piece_ml[e][my_head] = make_float2(m, sum);
+        if (lane == 0) sm.piece[e] = RowPiece{w.i, w.tile0, w.n_tiles, true};
     };
 
     // ---- the stream: groups g = 0, 1, ... of tiles t0, t0 + 1, ... ----
@@ -216,7 +229,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) decode_paged_rows_kernel(const
             if (gi == 0) {
                 const uint32_t t = t0 + g / kGroups, j = key_of(ahead, t);
                 const bool ok = page_ahead >= 0 && page_ahead < a.pc.n_pages;
-                row_issue = ok ? page_ahead * divide.rows + (j - divide.slot(j) * divide.rows) : -1;
+                row_issue = ok ? static_cast<int32_t>(page_ahead * divide.rows + (j - divide.slot(j) * divide.rows)) : -1;
                 if (!ok && j < ahead.n) {
                     wait_for_clear();
                     raise_flag(a.flag, TRI_FLAG_INDEX_RANGE);
@@ -240,12 +253,12 @@ __global__ void __launch_bounds__(kRowThreads, 1) decode_paged_rows_kernel(const
         }
         copy_commit();
     };
+    if (n_groups) begin_unit(cur.i);  // (while the first page entry is on its way)
     for (int g = 0; g < kRing; ++g) issue(g);
     // (The ring is at most one tile ahead, so the tile in use is the one
     // issued or the one before it.)
     uint32_t have_next = have_issue;
     static_assert(kRing <= kGroups, "ring longer than a tile");
-    if (n_groups) begin_unit(cur.i);
     for (uint32_t g = 0; g < n_groups; ++g) {
         const int gi = g % kGroups;
         if (gi == 0) {
@@ -365,43 +378,46 @@ __global__ void __launch_bounds__(kRowThreads, 1) decode_paged_rows_kernel(const
     }
     copy_wait<0>();
     if (n_groups) end_unit(cur);
-    // ---- the pieces, in the order of the warps; those of one unit follow one another ----
+    // ---- the pieces, in the order of the warps; those of one unit follow one
+    // another.  A warp takes a head of a unit: a lane has 4 dims. ----
     __syncthreads();
     SplitUnit split0 = {}, split1 = {};
-    int n_split = 0;
+    int n_split = 0, turn = 0;
 #pragma unroll 1
     for (int e0 = 0; e0 < 2 * kRowWarps;) {
-        if (!sm.piece[e0 >> 1][e0 & 1].any) {
+        const RowPiece w = sm.piece[e0];
+        if (!w.any) {
             ++e0;
             continue;
         }
-        const RowPiece w = sm.piece[e0 >> 1][e0 & 1];
         int e1 = e0 + 1;
-        while (e1 < 2 * kRowWarps && (!sm.piece[e1 >> 1][e1 & 1].any || sm.piece[e1 >> 1][e1 & 1].i == w.i)) ++e1;
+        while (e1 < 2 * kRowWarps && (!sm.piece[e1].any || sm.piece[e1].i == w.i)) ++e1;
         const bool whole = w.tile0 >= p.begin && w.tile0 + w.n_tiles <= p.end;
         const uint32_t slot = part_slot(p, blockIdx.x, w.tile0);
-        for (int e = tid; e < G * kD; e += kRowThreads) {
-            const int h = e / kD, d = e % kD;
-            float M = -INFINITY, num = 0.f, den = 0.f;
+#pragma unroll 1
+        for (int h = 0; h < G; ++h) {
+            if (turn++ % kRowWarps != warp) continue;
+            float M = -INFINITY;
+            for (int x = e0; x < e1; ++x)
+                if (sm.piece[x].any) M = fmaxf(M, sm.piece_ml[x][h].x);
+            const float base = M == -INFINITY ? 0.f : M;
+            float den = 0.f;
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
             for (int x = e0; x < e1; ++x) {
-                if (!sm.piece[x >> 1][x & 1].any) continue;
-                const float* f = (x & 1 ? reinterpret_cast<const float*>(sm.ring[x >> 1])
-                                        : a.pieces + (static_cast<int64_t>(blockIdx.x) * kRowWarps + (x >> 1)) * kPiece) +
-                                 h * (kD + 2);
-                const float m_new = fmaxf(M, f[0]);
-                const float base = m_new == -INFINITY ? 0.f : m_new;
-                const float fa = exp2f(M - base), fb = exp2f(f[0] - base);
-                num = fmaf(num, fa, fb * f[2 + d]);
-                den = fmaf(den, fa, fb * f[1]);
-                M = m_new;
+                if (!sm.piece[x].any) continue;
+                const float2 ml = sm.piece_ml[x][h];
+                const float f = exp2f(ml.x - base);
+                const float* from = x & 1 ? reinterpret_cast<const float*>(sm.ring[x >> 1])
+                                          : a.pieces + (static_cast<int64_t>(blockIdx.x) * kRowWarps + (x >> 1)) * kPiece;
+                den = fmaf(f, ml.y, den);
+                fma4(o, f, reinterpret_cast<const float4*>(from + h * kD)[lane]);
             }
             if (whole) {
-                const int64_t row = static_cast<int64_t>(w.i) * G + h;
-                a.out[row * kD + d] = den == 0.f ? 0.f : num / den;
-                if (a.lse && d == 0) a.lse[row] = lse_of(M, den);
+                write_joined(a, static_cast<int64_t>(w.i) * G + h, o, M, den);
             } else {
-                a.part[(static_cast<int64_t>(slot) * G + h) * kD + d] = num;
-                if (d == 0) a.part_ml[slot * G + h] = make_float2(M, den);
+                reinterpret_cast<float4*>(a.part + (static_cast<int64_t>(slot) * G + h) * kD)[lane] = o;
+                if (lane == 0) a.part_ml[slot * G + h] = make_float2(M, den);
             }
         }
         if (!whole) {
@@ -419,7 +435,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) decode_paged_rows_kernel(const
 // ---------------------------------------------------------------------------
 int decode_paged_ctas(int n_sm) { return n_sm; }
 
-size_t decode_paged_piece_bytes(int G) { return static_cast<size_t>(kRowWarps) * G * (kD + 2) * sizeof(float); }
+size_t decode_paged_piece_bytes(int G) { return kRowWarps * row_piece_floats(G) * sizeof(float); }
 
 cudaError_t launch_decode_paged_clear(const DecodePagedArgs& a, cudaStream_t s) {
     decode_clear_kernel<<<static_cast<unsigned>((a.sl.n + 255) / 256), 256, 0, s>>>(a.flag, a.counters,
@@ -431,7 +447,7 @@ cudaError_t launch_decode_paged_clear(const DecodePagedArgs& a, cudaStream_t s) 
 template <typename T, int G>
 static cudaError_t launch_rows(const DecodePagedArgs& a, int n_sm, cudaStream_t s) {
     constexpr size_t smem = sizeof(RowShared);
-    static_assert(row_piece_floats<G>() * 4 <= kRingBytes && smem <= 227 * 1024, "shared memory");
+    static_assert(row_piece_floats(G) * 4 <= kRingBytes && smem <= 227 * 1024, "shared memory");
     auto* fn = decode_paged_rows_kernel<T, G>;
     struct Key {};
     cudaError_t e = allow_smem<Key>(reinterpret_cast<const void*>(fn), smem);
