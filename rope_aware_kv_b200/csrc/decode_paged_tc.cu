@@ -485,7 +485,7 @@ decode_paged_tc_kernel(const __grid_constant__ CUtensorMap kmap,
         if (!ok) *reinterpret_cast<volatile int*>(&sm.failed) = 1;
         named_sync(1, kTcMath);
         if (!*reinterpret_cast<volatile int*>(&sm.failed))
-            join_split_units<kTcMath / 32, 1, 16>(a, G, n_split, split0, split1);
+            join_split_units<kTcMath / 32, 1, 32>(a, G, n_split, split0, split1);
     }
     wait_for_clear();
     write_empty_units(a, G);

@@ -396,7 +396,7 @@ __device__ void join_split_units(const DecodePagedArgs& a, int G, int n_split,
     // Head q: head q of the first unit that this CTA joins, or q - G of the other.
     const bool j0 = n_split > 0 && last[0], j1 = n_split > 1 && last[1];
     const int heads = (j0 ? G : 0) + (j1 ? G : 0);
-    constexpr int kAtOnce = kAhead / 4;
+    constexpr int kAtOnce = kAhead >= 16 ? 4 : 2;
 #pragma unroll 1
     for (int q0 = warp; q0 < heads; q0 += kWarps * kAtOnce) {
         SplitUnit s[kAtOnce];

@@ -13,9 +13,10 @@ def unit_list(n_seq, n_layers, n_kvheads, layer=-1):
             for h in range(n_kvheads)]
 
 
-def attention(q, k, v, scale):
+def attention(q, k, v, scale, dims=None):
     """q [G, D], k / v [n, D] float64 -> out [G, D], lse [G], and the error
-    bound of a float32 evaluation of each output.
+    bound of a float32 evaluation of each output.  (``dims``: v holds these
+    dims only.)
 
     The bound: a score is a sum of 128 products, each rounding of it at most
     2^-24 of the partial sum, at most A = scale sum |q_d k_d|; roundings of a
@@ -25,8 +26,9 @@ def attention(q, k, v, scale):
     exp2's 2^-22; the sums over the rows add 2^-24 a rounding, again as a
     random walk, taken 4 times.  The denominator is off by as much again."""
     G = q.shape[0]
-    out, lse = np.zeros((G, D)), np.full(G, -np.inf)
-    tol_o, tol_l = np.zeros((G, D)), np.zeros(G)
+    width = D if dims is None else len(dims)
+    out, lse = np.zeros((G, width)), np.full(G, -np.inf)
+    tol_o, tol_l = np.zeros((G, width)), np.zeros(G)
     n = len(k)
     if n == 0:
         return out, lse, tol_o, tol_l

@@ -241,6 +241,66 @@ def test_decode_graph_streams_and_shared_workspace():
     assert all(torch.equal(o, want) for o in outs)
 
 
+@pytest.mark.parametrize("dtype,page", [(BF16, 128), (BF16, 20), (F32, 64)])
+def test_decode_infinite_value_rows(dtype, page):
+    """An infinite value in a row of the cache makes that dim infinite in every
+    head that gives the row weight, and no other dim."""
+    n = 300
+    k, v, table, _ = _cache([n], page, dtype, 6)
+    q = torch.randn((1, 5, R.D), device=DEV, generator=torch.Generator(DEV).manual_seed(4)).to(dtype)
+    for j, d, x in ((0, 3, float("inf")), (150, 64, float("-inf")), (299, 127, float("inf"))):
+        v[int(table[0, j // page]), j % page, d] = x
+    out = tri.tri_decode_attention_paged(q, k, v, _i32(table), 1, 1, 1, _i32([n]))[0]
+    assert torch.all(out[:, [3, 127]] == float("inf")) and torch.all(out[:, 64] == float("-inf"))
+    rest = [d for d in range(R.D) if d not in (3, 64, 127)]
+    o, _, to, _ = R.attention(q[0].double().cpu().numpy(), _rows(k, table, 0, n).double().cpu().numpy(),
+                              _rows(v, table, 0, n).double().cpu().numpy()[:, rest], float(np.float32(R.D ** -0.5)), rest)
+    assert np.all(np.abs(out[:, rest].double().cpu().numpy() - o) <= to)
+
+
+@pytest.mark.parametrize("page", [64, 20])
+def test_far_rows(page):
+    """Rows whose elements lie past 2^31: attention, append, fit's copies and
+    compaction at the far end of a pool of 4.6 GB."""
+    n_pages = 18_000_000 // page
+    k = torch.empty((n_pages, page, R.D), dtype=BF16, device=DEV)
+    v = torch.empty_like(k)
+    n = 3 * page + 7
+    table = np.array([[n_pages - 1, n_pages - 5, 2, n_pages - 2, -1], [0, n_pages - 3, 1, n_pages - 4, -1]], np.int32)
+    g = torch.Generator(DEV).manual_seed(3)
+    for p in table[table >= 0]:
+        k[int(p)] = torch.randn((page, R.D), device=DEV, generator=g).to(BF16)
+        v[int(p)] = torch.randn((page, R.D), device=DEV, generator=g).to(BF16)
+    q = torch.randn((2, 4, R.D), device=DEV, generator=g).to(BF16)
+    _check_decode(q, k, v, table, [n, n - 1], 1, 1, 2)
+    # a third unit shares the first one's pages and gets copies of them
+    refs = torch.zeros(n_pages, dtype=torch.int32, device=DEV)
+    t = _i32(np.concatenate([table, table[:1]]))
+    refs.index_add_(0, t[t >= 0].long(), torch.ones(int((t >= 0).sum()), dtype=torch.int32, device=DEV))
+    refs[3:n_pages - 9] += (refs[3:n_pages - 9] == 0).int()  # only a few pages at each end are free
+    nv = _i32([n, n - 1, n])
+    free = tri.tri_pages_fit(k, v, t, refs, 3, nv, own=True)
+    assert free.item() == 4 - 4 and int(t[0].max()) == n_pages - 6  # the far free pages, lowest first
+    th = t.cpu().numpy()
+    for u in (0, 2):
+        assert torch.equal(_rows(k, th, 0, n), _rows(k, th, 2, n)) and torch.equal(_rows(v, th, 0, n), _rows(v, th, 2, n))
+    _check_decode(q, k, v, th[:2], [n, n - 1], 1, 1, 2)
+    kn = torch.randn((3, 2, R.D), device=DEV, generator=g).to(BF16)
+    want = [torch.cat([_rows(k, th, u, int(m)), kn[u]]) for u, m in enumerate([n, n - 1, n])]
+    tri.tri_append_paged(k, v, None, t, 3, 1, 1, nv, kn, kn, None, page_refs=refs)
+    assert nv.cpu().tolist() == [n + 2, n + 1, n + 2]
+    for u, m in enumerate([n + 2, n + 1, n + 2]):
+        assert torch.equal(_rows(k, th, u, m), want[u])
+    # most of the pool is freed, and what is left moves to its front
+    refs[3:n_pages - 9] = 0
+    refs.zero_().index_add_(0, t[t >= 0].long(), torch.ones(int((t >= 0).sum()), dtype=torch.int32, device=DEV))
+    live = tri.tri_pages_compact(k, v, t, refs)
+    assert live.item() == 12 and int(t.max()) == 11
+    for u, m in enumerate([n + 2, n + 1, n + 2]):
+        assert torch.equal(_rows(k, t.cpu().numpy(), u, m), want[u])
+    _check_decode(q, k, v, t.cpu().numpy()[:2], [n + 2, n + 1], 1, 1, 2)
+
+
 # ---------------------------------------------------------------------------
 # append
 # ---------------------------------------------------------------------------
@@ -472,6 +532,88 @@ def test_compact(U, page, ppu, n_pages, dtype):
         assert torch.equal(k, wk) and torch.equal(v, wv)
         assert tri.tri_pages_compact(k, None, t, c).item() == live  # nothing left to move
         assert np.array_equal(t.cpu().numpy(), ref.table) and torch.equal(k, wk)
+
+
+def test_fit_same_page_twice_in_a_unit():
+    """A page named by two slots of one unit, and by all slots of another."""
+    table = np.array([[0, 0, 1], [2, 2, 2]], np.int32)
+    refs = np.array([2, 1, 3, 0, 0, 0, 0], np.int32)
+    nv = np.array([11, 12], np.int32)
+    ref = R.Pages(table, refs, nv, 2, 4)
+    n_free = ref.fit([0, 0], own=True)
+    ref.check()
+    k = torch.randn((7, 4, R.D), device=DEV)
+    wk = k.clone()
+    for a, b, r in ref.copied:
+        wk[b, :r] = k[a, :r]
+    t, c = _i32(table), _i32(refs)
+    assert tri.tri_pages_fit(k, None, t, c, 2, _i32(nv), own=True).item() == n_free == 1
+    assert np.array_equal(t.cpu().numpy(), ref.table) and np.array_equal(c.cpu().numpy(), ref.refs)
+    assert torch.equal(k, wk)
+
+
+@pytest.mark.parametrize("n_new", [3, 30])
+def test_append_counts_out_of_range(n_new):
+    """n_add above n_new appends n_new rows, below 0 none; both are flagged."""
+    k, v, table, refs = _cache([100, 100, 100], 32, F32, 3, fill=0.0)
+    nv = _i32([10, 20, 30])
+    kn = torch.randn((3, n_new, R.D), device=DEV)
+    ws = tri.workspace(tri.tri_append_paged_workspace_bytes(3))
+    tri.tri_append_paged(k, v, None, _i32(table), 3, 1, 1, nv, kn, kn, None, n_add=_i32([n_new + 5, -2, 1]),
+                         page_refs=_i32(refs), ws=ws)
+    assert tri.tri_check_device_error(ws) == tri.FLAG_NVALID_RANGE
+    assert nv.cpu().tolist() == [10 + n_new, 20, 31]
+    assert torch.equal(_rows(k, table, 0, 10 + n_new)[10:], kn[0]) and torch.equal(_rows(v, table, 2, 31)[30:], kn[2, :1])
+
+
+def test_page_calls_captured():
+    """fit, append, attention, fork and compact of one step in a graph, on one
+    workspace and a side stream, replayed from two states: what the calls
+    give one by one."""
+    n_seq, L, H, page, ppu, n_pages = 4, 2, 2, 16, 8, 200
+    per, U = L * H, n_seq * L * H
+    states = [_state(n_seq, per, page, ppu, n_pages, seed, high=100) for seed in (1, 2)]
+    g = torch.Generator(DEV).manual_seed(5)
+    kn = torch.randn((U, 1, R.D), device=DEV, generator=g).to(BF16)
+    q = torch.randn((U, 2, R.D), device=DEV, generator=g).to(BF16)
+    k0 = torch.randn((n_pages, page, R.D), device=DEV, generator=g).to(BF16)
+    src, dst = _i32([0, 1, -1]), _i32([1, 0, 3])
+    k, v = k0.clone(), k0.clone()
+    t, c, nv = _i32(states[0][0]), _i32(states[0][1]), _i32(states[0][2])
+    out = torch.zeros((U, 2, R.D), device=DEV)
+    n_free, n_live = torch.zeros(1, dtype=torch.int32, device=DEV), torch.zeros(1, dtype=torch.int32, device=DEV)
+    ws = tri.workspace(max(tri.tri_pages_workspace_bytes(U, ppu, n_pages), tri.tri_append_paged_workspace_bytes(U),
+                           tri.tri_decode_paged_workspace_bytes(U, 2)))
+
+    def step():
+        tri.tri_pages_fit(k, v, t, c, n_seq, nv, n_new=1, n_free=n_free, ws=ws)
+        tri.tri_append_paged(k, v, None, t, n_seq, L, H, nv, kn, kn, None, page_refs=c, ws=ws)
+        tri.tri_decode_attention_paged(q, k, v, t, n_seq, L, H, nv, out=out, ws=ws)
+        tri.tri_pages_fork(t, c, page, n_seq, nv, src, dst, ws=ws)
+        tri.tri_pages_compact(k, v, t, c, n_live=n_live, ws=ws)
+
+    def start(state):
+        for x, y in zip((t, c, nv), state):
+            x.copy_(_i32(y))
+        k.copy_(k0)
+        v.copy_(k0)
+
+    want = []
+    for s in states:
+        start(s)
+        step()
+        want.append([x.clone() for x in (t, c, nv, k, v, out, n_free, n_live)])
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        step()
+    for s, w in list(zip(states, want)) * 2:
+        start(s)
+        graph.replay()
+        torch.cuda.synchronize()
+        for x, y in zip((t, c, nv, k, v, out, n_free, n_live), w):
+            assert torch.equal(x, y)
 
 
 # ---------------------------------------------------------------------------
