@@ -581,13 +581,20 @@ class _PagedCall:
 
     def check(self, name, t, dtype, shape):
         """t (None passes) is a contiguous tensor of this type and shape on the
-        call's device; a shape entry of -1 takes any size."""
-        if t is None:
-            return
-        if (t.dtype != dtype or t.get_device() != self.index or not t.is_contiguous()
-                or (t.shape != shape and (t.dim() != len(shape) or any(
-                    y not in (-1, x) for x, y in zip(t.shape, shape))))):
+        call's device."""
+        if t is not None and (t.shape != shape or t.dtype != dtype
+                              or t.get_device() != self.index or not t.is_contiguous()):
             self.refuse(name, t, dtype, shape)
+
+    def check_any(self, name, t, dtype, dims, at):
+        """The same with any size in dimension `at`; returns that size."""
+        if t is None:
+            return 0
+        if t.dim() != len(dims):
+            self.refuse(name, t, dtype, dims)
+        size = t.shape[at]
+        self.check(name, t, dtype, (*dims[:at], size, *dims[at + 1:]))
+        return size
 
     def refuse(self, name, t, dtype, shape):
         if t.dtype != dtype:
@@ -599,12 +606,14 @@ class _PagedCall:
         raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
 
     def pools(self, k_pool, v_pool):
-        if k_pool.dtype != torch.bfloat16:
+        dtype, shape = k_pool.dtype, k_pool.shape
+        if dtype != torch.bfloat16:
             _dt(k_pool)
-        self.check("k_pool", k_pool, k_pool.dtype, (-1, -1, -1))
-        if v_pool is not None:
-            self.check("v_pool", v_pool, k_pool.dtype, k_pool.shape)
-        self.n_pages, self.page_rows, self.d = k_pool.shape
+        if len(shape) != 3:
+            self.refuse("k_pool", k_pool, dtype, "of 3 dimensions")
+        self.check("k_pool", k_pool, dtype, shape)
+        self.check("v_pool", v_pool, dtype, shape)
+        self.n_pages, self.page_rows, self.d = shape
 
     def units(self, n_seq, n_layers, n_kvheads, layer):
         """Units of the call: all of them or one layer's."""
@@ -613,17 +622,17 @@ class _PagedCall:
                              f"{n_kvheads}")
         return self.n_units if layer < 0 else n_seq * n_kvheads
 
-    def empty(self, shape, dtype):
+    def empty(self, shape, dtype, like):
         """A buffer of the call's stream: it is not handed out again before the
         call is done with it."""
         if self.stream is None:
-            return torch.empty(shape, dtype=dtype, device=self.index)
+            return like.new_empty(shape, dtype=dtype)
         with torch.cuda.stream(self.stream):
-            return torch.empty(shape, dtype=dtype, device=self.index)
+            return like.new_empty(shape, dtype=dtype)
 
-    def run(self, name, nbytes, ws, args):
+    def run(self, name, nbytes, ws, like, args):
         if ws is None:
-            ws = self.empty(max(int(nbytes()), 256), torch.uint8)
+            ws = self.empty(max(int(nbytes()), 256), torch.uint8, like)
         elif ws.get_device() != self.index or not ws.is_contiguous():
             raise ValueError(f"ws must be a contiguous tensor on cuda:{self.index}")
         raw = (torch._C._cuda_getCurrentRawStream(self.index) if self.stream is None
@@ -663,16 +672,15 @@ def tri_decode_attention_paged(q: torch.Tensor, k_pool: torch.Tensor, v_pool: to
     layer = -1 if layer is None else int(layer)
     U = c.units(n_seq, n_layers, n_kvheads, layer)
     d = c.d
-    c.check("q", q, k_pool.dtype, (U, -1, d))
-    G = q.shape[1]
+    G = c.check_any("q", q, k_pool.dtype, (U, 0, d), 1)
     c.check("n_valid", n_valid, torch.int32, (c.n_units,))
     if out is None:
-        out = c.empty((U, G, d), torch.float32)
+        out = c.empty((U, G, d), torch.float32, q)
     else:
         c.check("out", out, torch.float32, (U, G, d))
     c.check("lse", lse, torch.float32, (U, G))
     sc = (1.0 / d ** 0.5) if scale is None else float(scale)
-    c.run("tri_decode_attention_paged", lambda: tri_decode_paged_workspace_bytes(U, G), ws,
+    c.run("tri_decode_attention_paged", lambda: tri_decode_paged_workspace_bytes(U, G), ws, q,
           (q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), _dt(k_pool), n_seq, n_layers,
            n_kvheads, layer, G, d, page_table.data_ptr(), c.page_rows, c.per_unit, c.n_pages,
            n_valid.data_ptr(), sc, out.data_ptr(), _p(lse)))
@@ -700,18 +708,17 @@ def tri_append_paged(k_pool: torch.Tensor, v_pool: Optional[torch.Tensor],
     c.pools(k_pool, v_pool)
     layer = -1 if layer is None else int(layer)
     U = c.units(n_seq, n_layers, n_kvheads, layer)
-    c.check("k_new", k_new, k_pool.dtype, (U, -1, c.d))
-    n_new = k_new.shape[1]
-    if v_new is not None:
-        c.check("v_new", v_new, k_pool.dtype, k_new.shape)
+    n_new = c.check_any("k_new", k_new, k_pool.dtype, (U, 0, c.d), 1)
+    c.check("v_new", v_new, k_pool.dtype, k_new.shape)
     c.check("pos_new", pos_new, torch.int32, (U, n_new))
-    c.check("pos", pos, torch.int32, (c.n_units, -1))
-    cap = c.per_unit * c.page_rows if pos is None else pos.shape[1]
+    cap = c.check_any("pos", pos, torch.int32, (c.n_units, 0), 1)
+    if pos is None:
+        cap = c.per_unit * c.page_rows
     c.check("n_valid", n_valid, torch.int32, (c.n_units,))
     c.check("n_add", n_add, torch.int32, (n_seq,))
     c.check("page_refs", page_refs, torch.int32, (c.n_pages,))
     c.check("p_cur", p_cur, torch.int64, (n_seq,))
-    c.run("tri_append_paged", lambda: tri_append_paged_workspace_bytes(U), ws,
+    c.run("tri_append_paged", lambda: tri_append_paged_workspace_bytes(U), ws, k_new,
           (k_pool.data_ptr(), _p(v_pool), _p(pos), _dt(k_pool), n_seq, n_layers, n_kvheads, layer,
            cap, c.d, page_table.data_ptr(), c.page_rows, c.per_unit, c.n_pages, _p(page_refs),
            n_valid.data_ptr(), _p(p_cur), k_new.data_ptr(), _p(v_new), _p(pos_new), _p(n_add),
@@ -738,11 +745,11 @@ def tri_pages_fit(k_pool: torch.Tensor, v_pool: Optional[torch.Tensor], page_tab
     c.check("n_valid", n_valid, torch.int32, (c.n_units,))
     c.check("n_add", n_add, torch.int32, (n_seq,))
     if n_free is None:
-        n_free = c.empty((1,), torch.int32)
+        n_free = c.empty((1,), torch.int32, n_valid)
     else:
         c.check("n_free", n_free, torch.int32, (1,))
     c.run("tri_pages_fit",
-          lambda: tri_pages_workspace_bytes(c.n_units, c.per_unit, c.n_pages), ws,
+          lambda: tri_pages_workspace_bytes(c.n_units, c.per_unit, c.n_pages), ws, page_refs,
           (k_pool.data_ptr(), _p(v_pool), _dt(k_pool), n_seq, c.n_units, c.d,
            page_table.data_ptr(), c.page_rows, c.per_unit, c.n_pages, page_refs.data_ptr(),
            n_valid.data_ptr(), _p(n_add), int(n_new), int(bool(own)), n_free.data_ptr()))
@@ -758,18 +765,16 @@ def tri_pages_fork(page_table: torch.Tensor, page_refs: torch.Tensor, page_rows:
     p_cur [n_seq] int64 follow.  Shared pages are copied by ``tri_pages_fit``
     when they are about to be written."""
     c = _PagedCall(page_table, stream)
-    c.check("page_refs", page_refs, torch.int32, (-1,))
-    n_pages = page_refs.shape[0]
+    n_pages = c.check_any("page_refs", page_refs, torch.int32, (0,), 0)
     c.check("n_valid", n_valid, torch.int32, (c.n_units,))
-    c.check("src_seq", src_seq, torch.int32, (-1,))
-    n_fork = src_seq.shape[0]
+    n_fork = c.check_any("src_seq", src_seq, torch.int32, (0,), 0)
     c.check("dst_seq", dst_seq, torch.int32, (n_fork,))
-    c.check("pos", pos, torch.int32, (c.n_units, -1))
+    cap = c.check_any("pos", pos, torch.int32, (c.n_units, 0), 1)
     c.check("p_cur", p_cur, torch.int64, (n_seq,))
-    c.run("tri_pages_fork", lambda: tri_pages_workspace_bytes(c.n_units, c.per_unit, n_pages), ws,
+    c.run("tri_pages_fork", lambda: tri_pages_workspace_bytes(c.n_units, c.per_unit, n_pages), ws, page_refs,
           (page_table.data_ptr(), int(page_rows), c.per_unit, n_pages, page_refs.data_ptr(), n_seq,
            c.n_units, src_seq.data_ptr(), dst_seq.data_ptr(), n_fork, n_valid.data_ptr(), _p(pos),
-           0 if pos is None else pos.shape[1], _p(p_cur)))
+           cap, _p(p_cur)))
 
 
 def tri_pages_compact(k_pool: torch.Tensor, v_pool: Optional[torch.Tensor],
@@ -783,11 +788,11 @@ def tri_pages_compact(k_pool: torch.Tensor, v_pool: Optional[torch.Tensor],
     c.pools(k_pool, v_pool)
     c.check("page_refs", page_refs, torch.int32, (c.n_pages,))
     if n_live is None:
-        n_live = c.empty((1,), torch.int32)
+        n_live = c.empty((1,), torch.int32, page_refs)
     else:
         c.check("n_live", n_live, torch.int32, (1,))
     c.run("tri_pages_compact",
-          lambda: tri_pages_workspace_bytes(c.n_units, c.per_unit, c.n_pages), ws,
+          lambda: tri_pages_workspace_bytes(c.n_units, c.per_unit, c.n_pages), ws, page_refs,
           (k_pool.data_ptr(), _p(v_pool), _dt(k_pool), c.n_units, c.d, page_table.data_ptr(),
            c.page_rows, c.per_unit, c.n_pages, page_refs.data_ptr(), n_live.data_ptr()))
     return n_live

@@ -712,7 +712,7 @@ cudaError_t launch_pages_fork(const ForkArgs& a, int n_sm, cudaStream_t s) {
     const int pos_jobs = static_cast<int>((pos_width + (int64_t(1) << pos_bits) - 1) >> pos_bits);
     constexpr size_t smem = (kForkCells + 3 * kMaxForks) * sizeof(int32_t);
     static_assert(smem <= 48 * 1024, "more than the default limit");
-    pages_fork_kernel<<<grid_for(per_seq * (table_jobs + pos_jobs), 1, 65535), kThreads, smem, s>>>(
+    pages_fork_kernel<<<grid_for(per_seq * (table_jobs + pos_jobs), 1, 5LL * n_sm), kThreads, smem, s>>>(
         a, table_bits, table_jobs, pos_bits, pos_jobs);
     note_launch(s);
     return cudaGetLastError();
