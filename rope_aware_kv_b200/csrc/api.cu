@@ -1276,7 +1276,11 @@ tri_status tri_decode_attention_paged(const void* q, const void* k_pool, const v
     a.pieces = reinterpret_cast<float*>(ws_at(ws, w.pieces));
     a.flag = ws_flag(ws);
     const int n_sm = static_cast<int>(sm_count_or_default());
-    // Whole 8-row swizzle atoms of a page can be loaded as tensor tiles.
+    // bf16 pages of whole 8-row swizzle atoms can be loaded as tensor tiles:
+    // 164 us against 189 us by the row kernel for 1.07 GB of rows and 1 head in
+    // pages of 128 rows, 194 against 321 us for 8 heads in pages of 8 rows, 54
+    // against 69 us for 1792 units of 130 rows.  (Units of 20 rows, which the
+    // host does not see, would take the row kernel 21 us and this one 40.)
     const int box = dt == TRI_BF16 ? decode_paged_box_rows(page_rows) : 0;
     CUtensorMap kmap, vmap;
     if (box) {
