@@ -564,9 +564,10 @@ cudaError_t launch_pages_fit(tri_dtype dt, const FitArgs& a, int n_sm, cudaStrea
 // read by some forks and replaced by another (beams that change places).  The
 // columns of the tables are independent of one another: a CTA takes some
 // columns of one (layer, head) for ALL forks, reads the sources' entries into
-// shared memory and only then writes the destinations'.  The
-// row counts of a (layer, head), which all its jobs read, are replaced by the
-// CTA that finishes the last of them.
+// shared memory and only then writes the destinations'.  Where a destination is
+// the source of another fork, the row counts of a (layer, head), which all its
+// jobs read, are replaced by the CTA that finishes the last of them; else by its
+// first job, without fences and atomics (31 against 34 us for 32 of 64 sequences).
 constexpr int kForkCells = 8192;  // entries that a CTA holds
 constexpr int kForkLoads = 4;
 
@@ -580,6 +581,7 @@ __global__ void __launch_bounds__(kThreads) pages_fork_kernel(const ForkArgs a, 
     int32_t* rows = dst + kMaxForks;   // rows of the source unit
     __shared__ bool last;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    bool crossed = false;  // a destination is the source of another fork
     const int F = static_cast<int>(a.n_fork);
     const int64_t per_seq = a.pc.n_units / a.pc.n_seq;  // (layer, head) pairs
     for (int f = tid; f < F; f += kThreads) {
@@ -609,6 +611,11 @@ __global__ void __launch_bounds__(kThreads) pages_fork_kernel(const ForkArgs a, 
         }
     }
     __syncthreads();
+    for (int f = tid; f < F; f += kThreads) {
+        if (src[f] == -2 || src[f] == dst[f]) continue;
+        for (int g = 0; g < F && !crossed; ++g) crossed = g != f && src[g] == dst[f];
+    }
+    crossed = __syncthreads_or(crossed);
     if (a.p_cur && blockIdx.x == 0) {
         int64_t now[kMaxForks / kThreads];
 #pragma unroll
@@ -682,19 +689,25 @@ __global__ void __launch_bounds__(kThreads) pages_fork_kernel(const ForkArgs a, 
                 }
             }
         }
-        // ---- the counts, when every job of the (layer, head) has read them ----
-        __syncthreads();
-        if (tid == 0) {
-            __threadfence();
-            last = atomicAdd(a.done + lh, 1u) == static_cast<uint32_t>(table_jobs + pos_jobs) - 1;
+        // ---- the counts: by the first job, or when every job of the (layer,
+        // head) has read them ----
+        if (crossed) {
+            __syncthreads();
+            if (tid == 0) {
+                __threadfence();
+                last = atomicAdd(a.done + lh, 1u) == static_cast<uint32_t>(table_jobs + pos_jobs) - 1;
+            }
+            __syncthreads();
+            if (!last) continue;
+        } else if (pos || col0 != 0) {
+            continue;
         }
         __syncthreads();
-        if (!last) continue;
         for (int f = tid; f < F; f += kThreads)
             cell[f] = src[f] >= 0 ? a.n_valid[src[f] * per_seq + lh] : 0;
         __syncthreads();
         for (int f = tid; f < F; f += kThreads)
-            if (src[f] != -2) a.n_valid[dst[f] * per_seq + lh] = cell[f];
+            if (src[f] != -2 && src[f] != dst[f]) a.n_valid[dst[f] * per_seq + lh] = cell[f];
     }
 }
 
@@ -702,13 +715,13 @@ cudaError_t launch_pages_fork(const ForkArgs& a, int n_sm, cudaStream_t s) {
     const int64_t per_seq = a.pc.n_units / a.pc.n_seq;
     // Columns of a job, a power of two: what fits the cells, but not so many
     // that the jobs leave the SMs (4 CTAs each) without work; 32 at least.
+    const int64_t pos_width = a.pos ? a.cap : 0;
     auto bits = [&](int64_t width) {
         int b = 5;
-        while ((int64_t(1) << b) < width && (width >> b) * per_seq > 4 * n_sm) ++b;
+        while ((int64_t(1) << b) < width && ((a.pc.per_unit + pos_width) >> b) * per_seq > 4 * n_sm) ++b;
         while (b > 0 && (a.n_fork << b) > kForkCells) --b;
         return b;
     };
-    const int64_t pos_width = a.pos ? a.cap : 0;
     const int table_bits = bits(a.pc.per_unit), pos_bits = bits(pos_width);
     const int table_jobs = static_cast<int>((a.pc.per_unit + (int64_t(1) << table_bits) - 1) >> table_bits);
     const int pos_jobs = static_cast<int>((pos_width + (int64_t(1) << pos_bits) - 1) >> pos_bits);
