@@ -583,6 +583,7 @@ size_t tri_append_paged_workspace_bytes(int64_t n_units);
  * padded batch past n_add[seq] are not read.
  *   v_pool with v_new, and pos ([n_units][cap]) with pos_new, may be NULL;
  *   cap <= pages_per_unit * page_rows bounds the rows of a unit.
+ *   n_add[seq] outside [0, n_new] is clamped (TRI_FLAG_NVALID_RANGE).
  *   page_refs (nullable): counts of tri_pages_fit; without them no page may
  *   be shared.
  * A unit whose rows do not fit in cap (TRI_FLAG_NVALID_RANGE), whose pages for
@@ -603,8 +604,8 @@ size_t tri_pages_workspace_bytes(int64_t n_units, int64_t pages_per_unit, int64_
 
 /*
  * Make every unit hold exactly the pages that its n_valid rows and the next
- * add = n_add[seq] rows (n_add NULL: n_new; n_add[seq] <= n_new) need, each
- * page that the next rows go into its own:
+ * add = n_add[seq] rows need (n_add NULL: n_new; outside [0, n_new]: clamped,
+ * TRI_FLAG_NVALID_RANGE), the pages that the next rows go into its own:
  *   1. pages of slots behind the last row are given back (entry -1, count - 1);
  *   2. slots without a page get one, and slots whose page is shared (count
  *      > 1) and holds a row >= n_valid[u] to be added get a copy of it, rows
