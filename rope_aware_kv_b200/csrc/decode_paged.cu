@@ -33,6 +33,9 @@
 
 namespace tri {
 
+// The attention starts while this runs (wait_for_clear): on the device it hides
+// behind the plan, where a memset in front of the kernel costs 0.5 to 1.3 us of
+// the calls of 25 us and more (and saves the host 1 us of 22).
 __global__ void __launch_bounds__(256) decode_clear_kernel(uint32_t* flag, uint32_t* counters, int64_t n) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int64_t i = blockIdx.x * 256ll + threadIdx.x;

@@ -27,8 +27,9 @@
 // Bound: K and V rows are read once (512 bytes a key), so HBM: 64 KB a tile
 // arrive in 1.5 us at an SM's share of it.  4 sequences x 8 heads of 98 to 131 K
 // rows (1.73 GB) take 255 us, 6.8 TB/s; 7168 units of 2176 rows 1.17 ms; 64 units
-// of about 2300 rows (76 MB) 25 us, of which 13 are ramp, join and launch.  With the products issued by one of
-// the four warps a tile took 1.8 us, and 1792 units of 130 rows 96 us.
+// of about 2300 rows (76 MB) 25 us, of which 13 are ramp, join and launch.  With
+// the products issued by one of the four warps a tile took 1.8 us, and 1792 units
+// of 130 rows 96 us (55 now).
 #include "paged_core.cuh"
 #include "tri_launch.h"
 

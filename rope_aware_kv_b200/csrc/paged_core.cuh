@@ -186,8 +186,10 @@ struct UnitCursor {
     __device__ int32_t page(const PageDivide& d, uint32_t j) const { return j < n ? pages[d.slot(j)] : -1; }
 };
 
-// The first kernel of the call clears the flag word and the counters and lets
-// the second one start at once; that one waits here before it touches them.
+// A kernel that was launched early (launch_early) waits here for the one before
+// it: the attention for the clearing of the flag word and the counters, before
+// it touches them.  Every warp of such a kernel does, else it could end, and
+// what follows it begin, before the other one is done.
 __device__ __forceinline__ void wait_for_clear() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // Let fn use `bytes` of dynamic shared memory; asked of the runtime once per

@@ -133,7 +133,6 @@ struct NewRows {
 // Few new rows a unit (what a warp's registers hold): one warp does all of a
 // unit, in one launch.  1792 units of 1 bf16 row: 8.5 us against 14.5 us by the
 // other two kernels, of 8 float32 rows 10.4 against 16.8 us; 448 units: alike.
-
 template <int kVec>
 __global__ void __launch_bounds__(kThreads) append_few_kernel(const AppendPagedArgs a) {
     const int lane = threadIdx.x & 31;
@@ -201,11 +200,13 @@ __global__ void __launch_bounds__(kThreads) append_copy_kernel(const AppendPaged
     const int64_t u = slice_unit(a.sl, i);
     const int64_t add = rows_added(a.n_add, u / (a.pc.n_units / a.pc.n_seq), a.n_new, nullptr);
     const int64_t x0 = (static_cast<int64_t>(blockIdx.x % chunks) * kWarps + warp) * kAppendFew;
-    if (x0 >= add) return;
-    const int m = static_cast<int>(min(add - x0, static_cast<int64_t>(kAppendFew)));
+    const int m = static_cast<int>(max(min(add - x0, static_cast<int64_t>(kAppendFew)), static_cast<int64_t>(0)));
     NewRows<kVec> rows;
     rows.read(a, i, x0, m, lane);
-    wait_for_clear();  // (here: for the look kernel)
+    // For the look kernel; by every warp, so that this kernel does not end
+    // before that one has.
+    wait_for_clear();
+    if (m == 0) return;
     const int64_t first = __ldcg(a.first + i);
     if (first >= 0) rows.write(a, u, first + x0, m, lane);
 }
