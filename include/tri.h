@@ -648,7 +648,8 @@ tri_status tri_pages_fork(int32_t* page_table, int64_t page_rows, int64_t pages_
  * Move the pool's n_live pages in use to its front: the i-th used page at or
  * behind n_live goes to the i-th free page before it, table entries and
  * counts follow, and pages n_live .. n_pages-1 are free afterwards (the pool
- * can be cut there).
+ * can be cut there).  Every table entry is looked at, whether or not a page
+ * moves; one that names no page of the pool is left as it is.
  *   v_pool: nullable.  n_live: out, nullable, device int32.
  */
 tri_status tri_pages_compact(void* k_pool, void* v_pool, tri_dtype dt, int64_t n_units,

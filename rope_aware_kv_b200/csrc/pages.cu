@@ -760,9 +760,8 @@ __global__ void __launch_bounds__(kGridThreads, 1) pages_compact_kernel(const Co
     const uint32_t below = sum_counts(a.counts, static_cast<uint32_t>(cl)).x + cta_sum(some);
     const int64_t moves = L - below;
     if (c == 0 && tid == 0 && a.n_live) *a.n_live = static_cast<int32_t>(L);
-    if (moves == 0) return;
     uint32_t base = sum.x;
-    for (int64_t b = p0; b < p1; b += kGridThreads) {
+    for (int64_t b = p0; b < p1 && moves > 0; b += kGridThreads) {
         const int64_t p = b + tid;
         const bool is_live = p < p1 && a.refs[p] != 0;
         uint32_t n;
@@ -776,12 +775,17 @@ __global__ void __launch_bounds__(kGridThreads, 1) pages_compact_kernel(const Co
         }
         base += n;
     }
-    if (!grid_barrier(a.barrier, 2, a.flag)) return;
-    // ---- the table entries that name the moving pages, their counts and rows ----
+    if (moves > 0 && !grid_barrier(a.barrier, 2, a.flag)) return;
+    // ---- the table entries that name the moving pages, their counts and rows
+    // (no page moves: the entries are only looked at) ----
     const int64_t slots = a.pc.n_units * a.pc.per_unit;
     for (int64_t id = c * kGridThreads + tid; id < slots; id += static_cast<int64_t>(gridDim.x) * kGridThreads) {
         const int64_t pg = a.pc.table[id];
-        if (pg < L || pg >= a.pc.n_pages) continue;
+        if (pg < -1 || pg >= a.pc.n_pages) {
+            raise_flag(a.flag, TRI_FLAG_INDEX_RANGE);
+            continue;
+        }
+        if (pg < L) continue;
         // An entry whose page's count is 0 names no listed page: left, flagged.
         const int64_t r = __ldcg(a.rank + pg);
         if (r >= 0 && r < moves && __ldcg(a.from + r) == pg)
