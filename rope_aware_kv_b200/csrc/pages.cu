@@ -685,7 +685,10 @@ __global__ void __launch_bounds__(kThreads) pages_fork_kernel(const ForkArgs a, 
                     }
                     if (now == old[q]) continue;
                     if (now >= 0) atomicAdd(a.refs + now, 1);
-                    if (old[q] >= 0 && old[q] < a.pc.n_pages) atomicSub(a.refs + old[q], 1);
+                    if (old[q] >= 0 && old[q] < a.pc.n_pages)
+                        atomicSub(a.refs + old[q], 1);
+                    else if (old[q] != -1)
+                        raise_flag(a.flag, TRI_FLAG_INDEX_RANGE);
                     to[c] = now;
                 }
             }

@@ -47,3 +47,22 @@ def test_compact_flags_bad_entries(moves):
     c = _i32(refs)
     tri.tri_pages_compact(want, None, t, c, ws=ws)
     assert tri.tri_check_device_error(ws) == 0
+
+
+@pytest.mark.parametrize("crossed", [False, True])
+def test_fork_flags_bad_entries_of_the_destination(crossed):
+    """An entry of a replaced sequence that names no page is dropped and
+    flagged; its valid entries give their pages back."""
+    page = 4
+    table = np.array([[0, 1, -1], [2, 9, -7], [3, -1, -1]], np.int32)
+    refs = _i32([1, 1, 1, 1, 0])
+    t, c, n = _i32(table), refs.clone(), _i32([6, 3, 4])
+    src, dst = ([0, 1], [1, 2]) if crossed else ([0], [1])
+    ws = tri.workspace(tri.tri_pages_workspace_bytes(3, 3, 5))
+    tri.tri_pages_fork(t, c, page, 3, n, _i32(src), _i32(dst), ws=ws)
+    assert tri.tri_check_device_error(ws) == tri.FLAG_INDEX_RANGE
+    assert t.cpu().tolist() == [[0, 1, -1], [0, 1, -1], [2, -1, -1] if crossed else [3, -1, -1]]
+    assert c.cpu().tolist() == ([2, 2, 1, 0, 0] if crossed else [2, 2, 0, 1, 0])
+    assert n.cpu().tolist() == [6, 6, 3 if crossed else 4]
+    tri.tri_pages_fork(t, c, page, 3, n, _i32(src), _i32(dst), ws=ws)  # nothing bad is left
+    assert tri.tri_check_device_error(ws) == 0
