@@ -633,7 +633,10 @@ tri_status tri_pages_fit(void* k_pool, void* v_pool, tri_dtype dt, int64_t n_seq
  * rows (count + 1; no row is copied: tri_pages_fit copies what will be
  * written), dst's old pages are given back, and n_valid, the first n_valid
  * positions of pos ([n_units][cap], nullable) and p_cur ([n_seq], nullable)
- * are copied.  src_seq[i] = -1 empties dst (n_valid and p_cur 0).
+ * are copied.  src_seq[i] = -1 empties dst (n_valid and p_cur 0).  A count of
+ * src outside [0, pages_per_unit * page_rows] is clamped, in what dst gets too
+ * (TRI_FLAG_NVALID_RANGE); bad entries of src's rows and of dst are dropped
+ * (TRI_FLAG_INDEX_RANGE).
  *   src_seq, dst_seq: device [n_fork] int32, n_fork <= 1024.
  * A fork with an index out of range, or whose dst_seq an earlier one has, is
  * skipped and sets TRI_FLAG_INDEX_RANGE.

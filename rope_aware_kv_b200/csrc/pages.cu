@@ -643,7 +643,7 @@ __global__ void __launch_bounds__(kThreads) pages_fork_kernel(const ForkArgs a, 
         const int cols = static_cast<int>(min(int64_t(1) << bits, width - col0));
         __syncthreads();
         for (int f = tid; f < F; f += kThreads)
-            rows[f] = src[f] < 0 ? 0 : clamp_nvalid(a.n_valid, src[f] * per_seq + lh, cap, nullptr);
+            rows[f] = src[f] < 0 ? 0 : clamp_nvalid(a.n_valid, src[f] * per_seq + lh, cap, a.flag);
         // A warp takes a fork at a time, its lanes neighbouring columns.  The
         // sources go straight to shared memory, all of them in flight, and
         // without waiting for their counts.
@@ -708,10 +708,12 @@ __global__ void __launch_bounds__(kThreads) pages_fork_kernel(const ForkArgs a, 
         }
         __syncthreads();
         for (int f = tid; f < F; f += kThreads)
-            cell[f] = src[f] >= 0 ? a.n_valid[src[f] * per_seq + lh] : 0;
+            cell[f] = src[f] >= 0 ? clamp_nvalid(a.n_valid, src[f] * per_seq + lh, cap, nullptr) : 0;
         __syncthreads();
+        // (A sequence that stays itself gets its clamped count, which is what
+        // every job reads of it before and after.)
         for (int f = tid; f < F; f += kThreads)
-            if (src[f] != -2 && src[f] != dst[f]) a.n_valid[dst[f] * per_seq + lh] = cell[f];
+            if (src[f] != -2) a.n_valid[dst[f] * per_seq + lh] = cell[f];
     }
 }
 

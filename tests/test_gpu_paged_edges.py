@@ -66,3 +66,26 @@ def test_fork_flags_bad_entries_of_the_destination(crossed):
     assert n.cpu().tolist() == [6, 6, 3 if crossed else 4]
     tri.tri_pages_fork(t, c, page, 3, n, _i32(src), _i32(dst), ws=ws)  # nothing bad is left
     assert tri.tri_check_device_error(ws) == 0
+
+
+@pytest.mark.parametrize("src,dst", [([0], [1]), ([0, 1], [1, 2]), ([0, 0], [0, 1]), ([1, 0], [0, 1])])
+def test_fork_clamps_row_counts(src, dst):
+    """A source's count past its pages' rows, or below 0, is clamped and
+    flagged, and the clamped count is what the destination gets."""
+    page, ppu = 4, 3
+    for bad, good in ((ppu * page + 7, ppu * page), (-5, 0)):
+        table = np.array([[0, 1, 2], [3, 4, -1], [5, -1, -1]], np.int32)
+        t, c = _i32(table), _i32([1, 1, 1, 1, 1, 1, 0])
+        n = np.array([bad, 6, 3], np.int32)
+        pos = np.arange(3 * 10, dtype=np.int32).reshape(3, 10)
+        ref = R.Pages(table, np.array([1, 1, 1, 1, 1, 1, 0], np.int32), np.array([good, 6, 3], np.int32), 3, page)
+        want_pos = pos.copy()
+        ref.fork(src, dst, want_pos)
+        nd, ps = _i32(n), _i32(pos)
+        ws = tri.workspace(tri.tri_pages_workspace_bytes(3, ppu, 7))
+        tri.tri_pages_fork(t, c, page, 3, nd, _i32(src), _i32(dst), pos=ps, ws=ws)
+        assert tri.tri_check_device_error(ws) == tri.FLAG_NVALID_RANGE
+        assert np.array_equal(t.cpu().numpy(), ref.table) and np.array_equal(c.cpu().numpy(), ref.refs)
+        assert np.array_equal(ps.cpu().numpy(), want_pos)
+        for s in dst:
+            assert nd[s].item() == ref.n_valid[s]
