@@ -457,8 +457,7 @@ static cudaError_t launch_rows(const DecodePagedArgs& a, int n_sm, cudaStream_t 
     constexpr size_t smem = sizeof(RowShared);
     static_assert(row_piece_floats(G) * 4 <= kRingBytes && smem <= 227 * 1024, "shared memory");
     auto* fn = decode_paged_rows_kernel<T, G>;
-    struct Key {};
-    cudaError_t e = allow_smem<Key>(reinterpret_cast<const void*>(fn), smem);
+    cudaError_t e = allow_smem(reinterpret_cast<const void*>(fn), smem);
     if (e != cudaSuccess) return e;
     e = launch_decode_paged_clear(a, s);
     if (e != cudaSuccess) return e;

@@ -512,8 +512,7 @@ static cudaError_t launch_tc(const CUtensorMap& kmap, const CUtensorMap& vmap, i
     constexpr size_t smem = sizeof(TcShared) + 1024;
     static_assert(smem <= 227 * 1024, "tile ring too large");
     auto* fn = decode_paged_tc_kernel<G>;
-    struct Key {};
-    cudaError_t e = allow_smem<Key>(reinterpret_cast<const void*>(fn), smem);
+    cudaError_t e = allow_smem(reinterpret_cast<const void*>(fn), smem);
     if (e != cudaSuccess) return e;
     e = launch_decode_paged_clear(a, s);
     if (e != cudaSuccess) return e;

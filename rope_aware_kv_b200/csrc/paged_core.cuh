@@ -1,8 +1,6 @@
 // paged_core.cuh -- device helpers of the paged-cache kernels.
 #pragma once
 
-#include <atomic>
-
 #include "paged.h"
 #include "tri_internal.cuh"
 
@@ -192,19 +190,11 @@ struct UnitCursor {
 // what follows it begin, before the other one is done.
 __device__ __forceinline__ void wait_for_clear() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
-// Let fn use `bytes` of dynamic shared memory; asked of the runtime once per
-// kernel (Key: a type that names it) and device.
-template <typename Key>
-cudaError_t allow_smem(const void* fn, size_t bytes) {
-    static std::atomic<uint64_t> done{0};
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
-    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
-    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
-    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
-    return e;
+// Let fn use `bytes` of dynamic shared memory.  Asked at every call, like the
+// other kernels': an answer kept from an earlier one would outlive the context
+// that it was given for (cudaDeviceReset).
+inline cudaError_t allow_smem(const void* fn, size_t bytes) {
+    return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
 }
 
 // Launch a kernel that may start before the previous one of the stream has

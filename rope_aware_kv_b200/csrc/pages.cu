@@ -398,12 +398,12 @@ __device__ __forceinline__ void copy_pages(void* k, void* v, int64_t copies, int
     bulk_wait_all();
 }
 
-template <typename Key, typename Args>
+template <typename Args>
 static cudaError_t launch_grid(void (*fn)(Args), const Args& a, int ctas, cudaStream_t s) {
     void* args[1] = {const_cast<Args*>(&a)};
     const void* f = reinterpret_cast<const void*>(fn);
     constexpr size_t smem = sizeof(CopyShared);
-    cudaError_t e = allow_smem<Key>(f, smem);
+    cudaError_t e = allow_smem(f, smem);
     if (e != cudaSuccess) return e;
     e = cudaLaunchCooperativeKernel(f, dim3(ctas), dim3(kGridThreads), args, smem, s);
     if (e == cudaSuccess) note_launch(s);
@@ -552,10 +552,8 @@ __global__ void __launch_bounds__(kGridThreads, 1) pages_fit_kernel(const FitArg
 int page_ctas(int n_sm) { return n_sm; }
 
 cudaError_t launch_pages_fit(tri_dtype dt, const FitArgs& a, int n_sm, cudaStream_t s) {
-    struct Bf16 {};
-    struct F32 {};
-    return dt == TRI_BF16 ? launch_grid<Bf16>(pages_fit_kernel<kD * 2>, a, page_ctas(n_sm), s)
-                          : launch_grid<F32>(pages_fit_kernel<kD * 4>, a, page_ctas(n_sm), s);
+    return dt == TRI_BF16 ? launch_grid(pages_fit_kernel<kD * 2>, a, page_ctas(n_sm), s)
+                          : launch_grid(pages_fit_kernel<kD * 4>, a, page_ctas(n_sm), s);
 }
 
 // ---------------------------------------------------------------------------
@@ -811,10 +809,8 @@ __global__ void __launch_bounds__(kGridThreads, 1) pages_compact_kernel(const Co
 
 cudaError_t launch_pages_compact(tri_dtype dt, const CompactPagesArgs& a, int n_sm,
                                  cudaStream_t s) {
-    struct Bf16 {};
-    struct F32 {};
-    return dt == TRI_BF16 ? launch_grid<Bf16>(pages_compact_kernel<kD * 2>, a, page_ctas(n_sm), s)
-                          : launch_grid<F32>(pages_compact_kernel<kD * 4>, a, page_ctas(n_sm), s);
+    return dt == TRI_BF16 ? launch_grid(pages_compact_kernel<kD * 2>, a, page_ctas(n_sm), s)
+                          : launch_grid(pages_compact_kernel<kD * 4>, a, page_ctas(n_sm), s);
 }
 
 }  // namespace tri

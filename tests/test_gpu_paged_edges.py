@@ -89,3 +89,46 @@ def test_fork_clamps_row_counts(src, dst):
         assert np.array_equal(ps.cpu().numpy(), want_pos)
         for s in dst:
             assert nd[s].item() == ref.n_valid[s]
+
+
+# One call of tri_pages_fit and one of each attention kernel through plain CUDA
+# runtime calls, before and after the device's context is made anew.
+_RESET = r"""
+import ctypes, sys
+import rope_aware_kv_b200 as tri
+lib = tri.load()
+P = ctypes.c_void_p
+rt = ctypes.CDLL(sys.argv[1])
+
+def buf(n):
+    p = P()
+    assert rt.cudaMalloc(ctypes.byref(p), ctypes.c_size_t(n)) == 0
+    assert rt.cudaMemset(p, 0, ctypes.c_size_t(n)) == 0
+    return p
+
+def calls():
+    big, small = [buf(1 << 20) for _ in range(4)], [buf(4096) for _ in range(4)]
+    q, k, v, ws = big
+    table, refs, n, out = small
+    got = [lib.tri_pages_fit(k, v, tri.TRI_BF16, 1, 1, 128, table, 8, 1, 4, refs, n, None, 1, 0, None, ws, 1 << 20, None)]
+    for rows in (8, 4):
+        wb = lib.tri_decode_paged_workspace_bytes(1, 1)
+        w = buf(wb)
+        got.append(lib.tri_decode_attention_paged(q, k, v, tri.TRI_BF16, 1, 1, 1, -1, 1, 128, table, rows, 1, 4, n,
+                                                  ctypes.c_float(0.1), out, None, w, wb, None))
+    got.append(rt.cudaDeviceSynchronize())
+    return got
+
+print(calls())
+assert rt.cudaDeviceReset() == 0
+print(calls())
+"""
+
+
+def test_calls_after_a_device_reset():
+    """A context made anew by cudaDeviceReset is followed (in a process of its
+    own, through the C entry points)."""
+    with open("/proc/self/maps") as f:
+        runtime = next(x.split()[-1] for x in f if "libcudart" in x)
+    r = subprocess.run([sys.executable, "-c", _RESET, runtime], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.split("\n")[:2] == ["[0, 0, 0, 0]"] * 2, (r.stdout, r.stderr[-2000:])
