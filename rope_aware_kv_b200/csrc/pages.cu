@@ -390,8 +390,13 @@ __device__ __forceinline__ void copy_pages(void* k, void* v, int64_t copies, int
             bulk_load_hint(window + (at - b0), pool + p.from * page_bytes + off, static_cast<uint32_t>(n), landed,
                            policy_evict_first());
         const bool ok = mbar_wait(landed, phase, flag);
+        if (!__all_sync(0xffffffffu, ok)) {
+            // Copies may still be in flight: once more (bounded as well), so
+            // that none lands in the window of a CTA that has ended.
+            mbar_wait(landed, phase, flag);
+            break;
+        }
         phase ^= 1;
-        if (!__all_sync(0xffffffffu, ok)) break;
         if (n > 0) bulk_store(pool + p.to * page_bytes + off, window + (at - b0), static_cast<uint32_t>(n));
         bulk_commit();
     }
