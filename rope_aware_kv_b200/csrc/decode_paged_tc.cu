@@ -274,6 +274,7 @@ decode_paged_tc_kernel(const __grid_constant__ CUtensorMap kmap,
             const uint64_t kd = tc_desc(sm.k, 16, kTcGroup, 2), qd = tc_desc(sm.q, 16, 1024, 2);
             const uint64_t vd = tc_desc(sm.v, kTcHalf, kTcGroup, 2), pd = tc_desc(sm.p, 16, 512, 4);
             uint32_t asked = 0;  // scores issued: of tiles 0 .. asked - 1
+            uint32_t given = 0;  // values issued
             auto scores = [&](uint32_t qb) {
                 const uint32_t x = asked++, stage = x % kTcStages;
                 if (!mbar_wait(&sm.k_full[stage], (x / kTcStages) & 1, a.flag)) return false;
@@ -297,9 +298,16 @@ decode_paged_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                 issue_values(vd + stage * (kTcMat >> 4), pd, o_cols);
                 tc_commit(&sm.o_full);
                 tc_commit(&sm.v_empty[stage]);
+                ++given;
                 if (asked == it + 1 && asked < n_it) ok = scores(w & 1);
                 if (ok && asked == it + 2 && (w & 2)) ok = scores(w & 1);
             }
+            // The products are done, and their last arrivals are in, before the
+            // CTA gives its tensor memory back and ends (also when a wait gave up).
+            for (uint32_t x = asked < kTcStages ? 0 : asked - kTcStages; x < asked; ++x)
+                mbar_wait(&sm.k_empty[x % kTcStages], (x / kTcStages) & 1, a.flag);
+            for (uint32_t x = given < kTcStages ? 0 : given - kTcStages; x < given; ++x)
+                mbar_wait(&sm.v_empty[x % kTcStages], (x / kTcStages) & 1, a.flag);
         }
         __syncwarp();
     } else {
