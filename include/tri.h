@@ -558,7 +558,8 @@ size_t tri_decode_paged_workspace_bytes(int64_t n_units, int G);
 /*
  * tri_decode_attention through the page table: attention of the next token
  * over each unit's first n_valid rows, split over the rows and joined.
- *   q: [units][G][head_dim] (dt); scale > 0; out: [units][G][head_dim] float32.
+ *   q: [units][G][head_dim] (dt); scale > 0, scale * log2(e) finite in float32;
+ *   out: [units][G][head_dim] float32.
  *   n_valid: [n_units], rows of every unit (pages_per_unit * page_rows at most).
  *   lse: out, nullable, [units][G] float32: log sum_j exp(s_j), -inf for a unit
  *   without rows (whose out is zeros), for joining with attention over other

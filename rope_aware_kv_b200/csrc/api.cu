@@ -1251,7 +1251,9 @@ tri_status tri_decode_attention_paged(const void* q, const void* k_pool, const v
     TRI_TRY(check_slice(n_seq, n_layers, n_kvheads, layer, &a.sl));
     const int64_t U = n_seq * n_layers * n_kvheads;
     TRI_TRY(check_paged(dt, head_dim, n_seq, U, page_table, page_rows, pages_per_unit, n_pages));
-    if (!q || !k_pool || !v_pool || !out || !n_valid || !(scale > 0.f) || !std::isfinite(scale))
+    // (The kernels take the scores in the base-2 logarithm.)
+    const float scale_log2 = scale * 1.4426950408889634f;
+    if (!q || !k_pool || !v_pool || !out || !n_valid || !(scale > 0.f) || !std::isfinite(scale_log2))
         return TRI_ERR_INVALID_ARG;
     if (G < 1 || G > TRI_MAX_GROUP) return TRI_ERR_UNSUPPORTED;
     if (!aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(out) ||
@@ -1267,7 +1269,7 @@ tri_status tri_decode_attention_paged(const void* q, const void* k_pool, const v
     a.v = v_pool;
     a.pc = paged_cache(page_table, page_rows, pages_per_unit, n_pages, n_seq, U);
     a.n_valid = n_valid;
-    a.scale_log2 = scale * 1.4426950408889634f;
+    a.scale_log2 = scale_log2;
     a.out = out;
     a.lse = lse;
     a.counters = reinterpret_cast<uint32_t*>(ws_at(ws, w.counters));

@@ -115,3 +115,13 @@ def test_sequential_tables_by_hand():
     assert p.fork([-1], [1]) == 0 and p.refs.tolist() == [1, 0, 1, 0, 0]
     assert p.compact() == 2 and p.table.tolist() == [[1, -1], [-1, -1], [0, -1]]
     p.check()
+
+
+def test_decode_refuses_a_scale_whose_base_2_form_overflows(lib):
+    """scale * log2(e) is what the scores are multiplied with: as infinity it
+    would turn a score of 0 into NaN."""
+    for scale in (2.4e38, 3.4e38):
+        with np.errstate(over="ignore"):
+            assert np.isfinite(np.float32(scale)) and np.isinf(np.float32(scale) * np.float32(1.4426950408889634))
+        assert _decode(lib, scale=scale) == 1
+    assert _decode(lib, scale=2.3e38, ws=None) == 3
