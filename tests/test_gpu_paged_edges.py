@@ -132,3 +132,65 @@ def test_calls_after_a_device_reset():
         runtime = next(x.split()[-1] for x in f if "libcudart" in x)
     r = subprocess.run([sys.executable, "-c", _RESET, runtime], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and r.stdout.split("\n")[:2] == ["[0, 0, 0, 0]"] * 2, (r.stdout, r.stderr[-2000:])
+
+
+@pytest.mark.parametrize("n_seq,per_seq,page,ppu,n_fork,seed", [
+    (8, 6, 16, 40, 4, 0), (12, 5, 4, 300, 7, 1), (64, 8, 16, 130, 32, 2), (700, 2, 8, 30, 600, 3),
+    (2048, 1, 8, 20, 1024, 4), (1024, 1, 4, 70, 1024, 5)])
+def test_fork_of_sequences_that_are_only_read(n_seq, per_seq, page, ppu, n_fork, seed):
+    """Forks none of whose destinations is another fork's source: repeated
+    sources, emptied sequences, sequences that stay themselves, over several
+    (layer, head) pairs and more columns than one job takes."""
+    n_pages = n_seq * per_seq * ppu + 3
+    cap = ppu * page - 1
+    table, refs, nv = _state(n_seq, per_seq, page, ppu, n_pages, seed, high=cap)
+    for u in range(len(nv)):  # rows whose pages are there
+        nv[u] = min(int(nv[u]), page * int((table[u] >= 0).sum()), cap)
+    rng = np.random.default_rng(seed + 70)
+    order = rng.permutation(n_seq)
+    only_read, dst = order[:n_seq - n_fork], order[n_seq - n_fork:].copy()
+    if len(only_read):
+        src = rng.choice(only_read, n_fork)
+        src[0] = src[-1]
+    else:  # every sequence is a destination: all stay themselves or are emptied
+        src = dst.copy()
+    src[rng.random(n_fork) < 0.15] = -1
+    stays = rng.random(n_fork) < 0.2
+    src[stays] = dst[stays]
+    for f in range(n_fork):
+        assert src[f] == dst[f] or dst[f] not in src
+    assert len(set(dst.tolist())) == n_fork
+    pos = rng.integers(0, 30000, (n_seq * per_seq, cap)).astype(np.int32)
+    p_cur = rng.integers(0, 30000, n_seq).astype(np.int64)
+    ref = R.Pages(table, refs, nv, n_seq, page)
+    wpos, wcur = pos.copy(), p_cur.copy()
+    assert ref.fork(src.tolist(), dst.tolist(), wpos, wcur) == 0
+    ref.check()
+    ws = tri.workspace(tri.tri_pages_workspace_bytes(*table.shape, n_pages))
+    for _ in range(3):
+        t, c, n, ps = _i32(table), _i32(refs), _i32(nv), _i32(pos)
+        pc = torch.as_tensor(p_cur, device=DEV)
+        tri.tri_pages_fork(t, c, page, n_seq, n, _i32(src), _i32(dst), pos=ps, p_cur=pc, ws=ws)
+        assert tri.tri_check_device_error(ws) == 0
+        assert np.array_equal(t.cpu().numpy(), ref.table) and np.array_equal(c.cpu().numpy(), ref.refs)
+        assert np.array_equal(n.cpu().numpy(), ref.n_valid)
+        assert np.array_equal(ps.cpu().numpy(), wpos) and np.array_equal(pc.cpu().numpy(), wcur)
+
+
+def test_fork_1024_crossed():
+    """The most forks of one call, every destination the next one's source."""
+    n_seq, page, ppu = 1024, 4, 40
+    n_pages = n_seq * ppu + 3
+    table, refs, nv = _state(n_seq, 1, page, ppu, n_pages, 9, high=ppu * page)
+    for u in range(n_seq):
+        nv[u] = min(int(nv[u]), page * int((table[u] >= 0).sum()))
+    dst = np.random.default_rng(1).permutation(n_seq)
+    src = np.roll(dst, 1)
+    ref = R.Pages(table, refs, nv, n_seq, page)
+    assert ref.fork(src.tolist(), dst.tolist()) == 0
+    t, c, n = _i32(table), _i32(refs), _i32(nv)
+    ws = tri.workspace(tri.tri_pages_workspace_bytes(*table.shape, n_pages))
+    tri.tri_pages_fork(t, c, page, n_seq, n, _i32(src), _i32(dst), ws=ws)
+    assert tri.tri_check_device_error(ws) == 0
+    assert np.array_equal(t.cpu().numpy(), ref.table) and np.array_equal(c.cpu().numpy(), ref.refs)
+    assert np.array_equal(n.cpu().numpy(), ref.n_valid)
