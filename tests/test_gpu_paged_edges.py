@@ -194,3 +194,124 @@ def test_fork_1024_crossed():
     assert tri.tri_check_device_error(ws) == 0
     assert np.array_equal(t.cpu().numpy(), ref.table) and np.array_equal(c.cpu().numpy(), ref.refs)
     assert np.array_equal(n.cpu().numpy(), ref.n_valid)
+
+
+def _exact_scores(n, G, page, dtype, seed):
+    """One unit of n rows whose scores are whole numbers times 2^-8 in any
+    order of summation; every 32 rows hold each head's largest score at their
+    front, so the running maximum never changes and no weight is rescaled; and V has one
+    row a dim, whose element is 1, so out[h, d] is one row's weight over the
+    sum of all.  Returns q, k, v, table and the dims' rows."""
+    rng = np.random.default_rng(seed)
+    q = rng.choice([-2, -1, 1, 2], (G, R.D))
+    kk = rng.integers(-2, 3, (n, R.D))
+    tops = [j0 + h for j0 in range(0, n, 32) for h in range(G)]
+    for j in tops:
+        if j < n:
+            kk[j] = 2 * np.sign(q[j % 32])
+    s = kk @ q.T
+    assert all(s[j0 + h, h] == s[:, h].max() for j0 in range(0, n, 32) for h in range(G)
+               if j0 + h < n)
+    rest = np.setdiff1d(np.arange(n), tops)
+    dims = min(len(rest), R.D)
+    at = np.sort(rng.choice(rest, dims, replace=False))
+    k, v, table, _ = _cache([n], page, dtype, seed)
+    for j in range(n):
+        v[int(table[0, j // page]), j % page] = 0.0
+        k[int(table[0, j // page]), j % page] = torch.as_tensor(kk[j], device=DEV).to(dtype)
+    for d, j in enumerate(at):
+        v[int(table[0, j // page]), j % page, d] = 1.0
+    return torch.as_tensor(q[None], device=DEV).to(dtype), k, v, table, s, at
+
+
+@pytest.mark.parametrize("dtype,page,n", [(BF16, 128, 128), (BF16, 8, 100), (BF16, 64, 640), (BF16, 128, 1280),
+                                          (BF16, 20, 128), (BF16, 20, 640), (F32, 64, 128), (F32, 24, 1280)])
+@pytest.mark.parametrize("G", [1, 7, 8])
+def test_decode_weights_are_float32(dtype, page, n, G):
+    """Each weight by itself.  With exact scores a weight over the sum is off by
+
+      exp2: 2 ulp, at most 4 eps (eps = 2^-24, half an ulp's most);
+      its argument x = s scale log2(e) - max, 0 >= x > -4: one rounding of at
+        most 2^-23, times ln 2: 1.4 eps; log2(e) is off by 1.4e-8 of itself,
+        times 4 ln 2: 0.7 eps;
+      the split into three bf16 terms 2^-27, and the sum of the terms, the
+        accumulator, the reciprocal and the product with it, a rounding each:
+        4.2 eps;
+      the sum of the weights: the same factor for every row of a head.
+
+    So but for that factor at most 10.3 eps, and their root mean square no more.
+    Weights in two terms of bf16, on the same scores, are off by three times
+    that."""
+    eps = 2.0 ** -24
+    q, k, v, table, s, at = _exact_scores(n, G, page, dtype, 100 * G + n + page)
+    scale = 2.0 ** -8
+    x = (s - s.max(0)) * scale / np.log(2.0)
+    assert x.min() > -4
+    p = np.exp2(x)
+    one = torch.as_tensor(p).bfloat16().double()
+    two = one + (torch.as_tensor(p) - one).bfloat16().double()
+    assert np.sqrt(((two.numpy() / p - 1)[at] ** 2).mean()) > 25 * eps
+    want = (p / p.sum(0))[at].T
+    out = tri.tri_decode_attention_paged(q, k, v, _i32(table), 1, 1, 1, _i32([n]), scale=scale)[0].double().cpu().numpy()
+    dims = len(at)
+    assert not out[:, dims:].any()
+    rel = out[:, :dims] / want - 1
+    own = rel - rel.mean(1, keepdims=True)
+    # The factor: the weights' own bound twice (in the sum, and the mean of
+    # these), and a rounding for each of at most n / 4 + 40 steps of a sum.
+    assert np.abs(rel.mean(1)).max() <= (2 * 10.3 + n / 4 + 40) * eps
+    assert np.abs(own).max() <= 2 * 10.3 * eps
+    assert np.sqrt((own ** 2).mean()) <= 10.3 * eps
+
+
+@pytest.mark.parametrize("dtype,page", [(BF16, 128), (BF16, 64), (BF16, 20), (F32, 64)])
+@pytest.mark.parametrize("n", [3, 130, 1025, 9000])
+def test_decode_error_next_to_plain_float32(dtype, page, n):
+    """The relative error (Euclidean, over all units) is at most 4 times that of
+    elementary float32 operations.  The kernels round no more often than those;
+    a tensor-core sum that truncates errs to one side, 2 eps a step of 16
+    products: 8 steps, 16 eps of a score's partial sums, where 128 roundings
+    add up to sqrt(128) eps / sqrt(3) = 6.5 eps: 2.5 times; and likewise for the
+    8 steps of a tile's values."""
+    U, G = 6, 4
+    k, v, table, _ = _cache([n] * U, page, dtype, n + page)
+    q = (torch.randn((U, G, R.D), device=DEV, generator=torch.Generator(DEV).manual_seed(n)) * 2).to(dtype)
+    out = tri.tri_decode_attention_paged(q, k, v, _i32(table), 1, 1, U, _i32([n] * U))
+    assert not torch.backends.cuda.matmul.allow_tf32
+    err, plain, size = 0.0, 0.0, 0.0
+    for u in range(U):
+        kr, vr = _rows(k, table, u, n), _rows(v, table, u, n)
+        x = q[u].double() @ kr.double().T * R.D ** -0.5
+        want = torch.softmax(x, 1) @ vr.double()
+        y = (q[u].float() @ kr.float().T) * R.D ** -0.5
+        w = torch.exp(y - y.amax(1, keepdim=True))
+        ours = (w @ vr.float()) / w.sum(1, keepdim=True)
+        err += ((out[u].double() - want) ** 2).sum().item()
+        plain += ((ours.double() - want) ** 2).sum().item()
+        size += (want ** 2).sum().item()
+    assert err ** 0.5 <= 4 * plain ** 0.5, (err / size, plain / size)
+
+
+@pytest.mark.parametrize("dtype,page", [(BF16, 128), (BF16, 20), (F32, 64)])
+@pytest.mark.parametrize("n", [129, 400])
+def test_decode_huge_values_without_weight(dtype, page, n):
+    """Values of 1e38 in rows whose weight is 0 in float32, the last of them
+    alone in its tile, leave nothing in the output."""
+    G = 4
+    k, v, table, _ = _cache([n], page, dtype, n)
+    q = torch.randn((1, G, R.D), device=DEV, generator=torch.Generator(DEV).manual_seed(4)).to(dtype)
+    away = -30.0 * q[0].float().sum(0)
+    for x, j in enumerate((0, n // 2, n - 1)):
+        k[int(table[0, j // page]), j % page] = away.to(dtype)
+        v[int(table[0, j // page]), j % page] = (torch.full((R.D,), 1e38, device=DEV) * (-1) ** x).to(dtype)
+    gone = (0, n // 2, n - 1)
+    s = (q[0].double() @ _rows(k, table, 0, n).double().T * R.D ** -0.5).cpu().numpy()
+    for j in gone:
+        assert np.all(s[:, j] < s.max(1) - 110)  # exp(-110) < 2^-158, below float32's least 2^-149
+    keep = [j for j in range(n) if j not in gone]
+    lse = torch.zeros((1, G), device=DEV)
+    out = tri.tri_decode_attention_paged(q, k, v, _i32(table), 1, 1, 1, _i32([n]), lse=lse)
+    o, ls, to, tl = R.attention(q[0].double().cpu().numpy(), _rows(k, table, 0, n).double().cpu().numpy()[keep],
+                                _rows(v, table, 0, n).double().cpu().numpy()[keep], float(np.float32(R.D ** -0.5)))
+    assert np.all(np.abs(out[0].double().cpu().numpy() - o) <= to)
+    assert np.all(np.abs(lse[0].double().cpu().numpy() - ls) <= tl)
