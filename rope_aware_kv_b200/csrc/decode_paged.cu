@@ -151,8 +151,10 @@ __global__ void __launch_bounds__(kRowThreads, 1) decode_paged_rows_kernel(const
                 rows = __shfl_sync(0xffffffffu, n, w);
                 break;
             }
+            // (Unit i + 32 has not been looked at: it is among the next 32.)
             tile0 += __shfl_sync(0xffffffffu, incl, 31);
             i += 32;
+            rows = 0;
         }
         cur.first(a, i, tile0, rows, t1);
     }

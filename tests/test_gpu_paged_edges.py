@@ -11,7 +11,7 @@ import torch
 import rope_aware_kv_b200 as tri
 from rope_aware_kv_b200 import build as tri_build
 from tests import paged_ref as R
-from tests.test_gpu_paged import BF16, DEV, F32, _cache, _i32, _rows, _state
+from tests.test_gpu_paged import BF16, DEV, F32, _cache, _check_decode, _i32, _rows, _state
 
 pytestmark = pytest.mark.gpu
 
@@ -315,3 +315,27 @@ def test_decode_huge_values_without_weight(dtype, page, n):
                                 _rows(v, table, 0, n).double().cpu().numpy()[keep], float(np.float32(R.D ** -0.5)))
     assert np.all(np.abs(out[0].double().cpu().numpy() - o) <= to)
     assert np.all(np.abs(lse[0].double().cpu().numpy() - ls) <= tl)
+
+
+def _many_units(kind):
+    rng = np.random.default_rng(7)
+    if kind == "0 or 1":
+        return np.repeat(rng.integers(0, 2, 52), 8)
+    if kind == "one in 40":
+        return np.where(rng.random(2000) < 1 / 40, rng.integers(1, 33, 2000), 0)
+    if kind == "short":
+        return rng.integers(0, 41, 6000)
+    n = np.where(rng.random(3000) < 1 / 15, rng.integers(1, 300, 3000), 0)
+    n[[0, 40, 41, 700, 2999]] = [900, 0, 33, 1300, 64]
+    return n
+
+
+@pytest.mark.parametrize("dtype,page", [(F32, 32), (F32, 24), (BF16, 20), (BF16, 128)])
+@pytest.mark.parametrize("kind", ["0 or 1", "one in 40", "short", "gaps"])
+def test_decode_ranges_of_many_units(kind, dtype, page):
+    """A CTA's range that spans more units than a warp looks at at once: many
+    short ones, or long stretches of units without a row."""
+    n = _many_units(kind).astype(np.int32)
+    k, v, table, _ = _cache(n, page, dtype, 3)
+    q = torch.randn((len(n), 3, R.D), device=DEV, generator=torch.Generator(DEV).manual_seed(5)).to(dtype)
+    _check_decode(q, k, v, table, n, 1, 1, len(n))
