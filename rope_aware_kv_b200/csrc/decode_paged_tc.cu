@@ -24,12 +24,18 @@
 // has just asked for; a unit's Q, row count and page entries are read while
 // the unit before it is worked on.
 //
-// Bound: K and V rows are read once (512 bytes a key), so HBM: 64 KB a tile
-// arrive in 1.5 us at an SM's share of it.  4 sequences x 8 heads of 98 to 131 K
-// rows (1.73 GB) take 255 us, 6.8 TB/s; 7168 units of 2176 rows 1.17 ms; 64 units
-// of about 2300 rows (76 MB) 25 us, of which 13 are ramp, join and launch.  With
-// the products issued by one of the four warps a tile took 1.8 us, and 1792 units
-// of 130 rows 96 us (55 now).
+// Bound: K and V are read once (512 bytes a key), so HBM: 64 KB a tile arrive in
+// 1.5 us at an SM's share of it.  4 sequences x 8 heads of 98 to 131 K rows (1.73
+// GB) take 258 us, 6.7 TB/s; 7168 units of 2176 rows 1.17 ms; 64 units of about
+// 2300 rows (76 MB) 25 us, of which 13 are ramp, join and launch.  What is read
+// is whole boxes (the largest power of two of rows, 128 at most, that divides a
+// page), so a unit's last box brings rows behind its end too: 1792 units of 130
+// rows in pages of 128 read 237 MB for 119 MB of rows.  That is the smaller part
+// of what short units lose: they take 56 us, and 50 in pages of 8 rows (125 MB);
+// 20 rows a unit 42 and 38.  The rest is what a tile costs that is its unit's
+// only one (weights, values and results one after the other).  With the products
+// issued by one of the four warps a tile took 1.8 us, and 1792 units of 130 rows
+// 96 us.
 #include "paged_core.cuh"
 #include "tri_launch.h"
 

@@ -572,6 +572,11 @@ cudaError_t launch_pages_fit(tri_dtype dt, const FitArgs& a, int n_sm, cudaStrea
 // the source of another fork, the row counts of a (layer, head), which all its
 // jobs read, are replaced by the CTA that finishes the last of them; else by its
 // first job, without fences and atomics (31 against 34 us for 32 of 64 sequences).
+// Every CTA looks all forks over by itself, each fork against the others, and the
+// columns of a job are 8192 / n_fork: right for a batch of sequences, while from a
+// few hundred forks on both cost more than the tables.  3584 units of 16 entries
+// take 9 us as 32 forks, 42 as 256, 105 as 512, 305 as 1024; with positions of 2048
+// rows a unit and 28 (layer, head) pairs 1024 forks take 2.05 ms (floor 78 us).
 constexpr int kForkCells = 8192;  // entries that a CTA holds
 constexpr int kForkLoads = 4;
 
@@ -726,8 +731,8 @@ __global__ void __launch_bounds__(kThreads) pages_fork_kernel(const ForkArgs a, 
 
 cudaError_t launch_pages_fork(const ForkArgs& a, int n_sm, cudaStream_t s) {
     const int64_t per_seq = a.pc.n_units / a.pc.n_seq;
-    // Columns of a job, a power of two: what fits the cells, but not so many
-    // that the jobs leave the SMs (4 CTAs each) without work; 32 at least.
+    // Columns of a job, a power of two: as few as leave an SM at most 4 jobs
+    // (5 CTAs fit it), 32 at least, and no more than fit the cells.
     const int64_t pos_width = a.pos ? a.cap : 0;
     auto bits = [&](int64_t width) {
         int b = 5;
